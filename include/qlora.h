@@ -369,6 +369,111 @@ int qlora_linear_bwd_dropout(const qlora_nf4_desc* d, const uint8_t* packed, con
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * 8-bit forms
+ * -----------
+ * The 8-bit form of a matrix M [rows][cols] (cols a multiple of 64): one
+ * e4m3 code per element (OCP: largest finite value 448, 0x7F and 0xFF NaN)
+ * and one power-of-two scale 2^(e - 127), kept as the byte e, per block of
+ * block_rows x 128 elements, block_rows being 1 (layer inputs, gradients) or
+ * 128 (weights).  The last block of a row, and the last row of blocks, may be
+ * short.
+ *   codes  [rows][cols] uint8
+ *   scales [ceil(rows / block_rows)][4 ceil(cols / 512)] uint8: the row's
+ *          ceil(cols / 128) bytes e, then bytes 127 up to whole dwords
+ * e is the smallest byte in 1 .. 254 with
+ *   (largest finite |x| of the block) <= 448 * 2^(e - 127)
+ * and code = e4m3(x * 2^(127 - e)), rounded to nearest even (exact scaling,
+ * one rounding); an element that is not finite becomes a NaN code and takes
+ * no part in the largest.  Rows keep their own scales, so a range of rows of
+ * a form by rows is the form of those rows.
+ *
+ * One form serves twice.  It is the checkpoint of a layer's input for the
+ * backward pass, at half the memory of bf16 ("LoRA 与 QLoRA：..." §7, §10:
+ * activations are what grows with the context; checkpointing trades them for
+ * compute): qlora_linear_bwd_checkpoint and qlora_fp8_linear_bwd take it
+ * where qlora_linear_bwd takes X.  And it is the operand of the products of a
+ * layer whose frozen weight is kept at 8 bits (block_rows 128).
+ *
+ * codes and M are 16-byte aligned, scales 4-byte aligned;
+ * rows * ceil(cols / 512) < 2^27.
+ * Scales other than 1 .. 254 are not produced; results for them are
+ * unspecified.
+ */
+int qlora_fp8_sizes(int64_t rows, int64_t cols, int32_t block_rows, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * M [rows][cols] (device; m_format QLORA_W_F32, QLORA_W_BF16 or QLORA_W_F16)
+ * -> codes, scales (device, sizes from qlora_fp8_sizes).  rows == 0 does
+ * nothing.  Bit-exact and deterministic.
+ * Errors: NULL, SHAPE, UNSUPPORTED (block_rows, m_format, alignment), HIP.
+ */
+int qlora_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const void* M, int32_t m_format,
+                       uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * codes, scales -> M_hat [rows][cols] bf16 = bf16_rne(code * 2^(e - 127)).
+ * Exact wherever the value is a normal bf16 (e >= 8 suffices).  For a layer
+ * input that is recomputed from, and for export of an 8-bit weight.
+ * Errors: NULL, SHAPE, UNSUPPORTED (block_rows, alignment), HIP.
+ */
+int qlora_dequantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const uint8_t* codes, const uint8_t* scales,
+                         uint16_t* M_hat, void* stream);
+
+/*
+ * Forward of a layer whose frozen weight W [d_out][d_in] is kept in the 8-bit
+ * form (block_rows 128) and whose input is in the 8-bit form by rows:
+ *   U = X_hat A^T (fp32 [T][r]),  Y = bf16( X_hat W_hat^T + s U B^T )
+ * X_hat, W_hat being the values the forms stand for.  A [r][d_in], B
+ * [d_out][r], Y [T][d_out] bf16; U_out (fp32 [T][r]) may be NULL; r == 0 (A, B
+ * NULL) is the base product alone.  Sums are fp32, except that the matrix
+ * units add the products of eight consecutive (in their order) codes aligned
+ * to the largest of the eight, which drops what is below 2^-13 of it.
+ * Deterministic.  Size limits, alignment and errors as qlora_linear_fwd (the
+ * weight's codes in place of the packed weight; scales 4-byte aligned); the
+ * workspace is 16-byte aligned.
+ */
+int qlora_fp8_fwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t T, int32_t r, size_t* bytes);
+int qlora_fp8_linear_fwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, const uint8_t* W_scales, int64_t T,
+                         const uint8_t* X_codes, const uint8_t* X_scales, int32_t r, float alpha, const uint16_t* A,
+                         const uint16_t* B, uint16_t* Y, float* U_out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Its backward (dY [T][d_out] bf16):
+ *   G  = dY B
+ *   dX = bf16( dY_hat W_hat + s G A )     dY_hat: the 8-bit form of dY by rows
+ *   dA = s G^T X_hat   fp32 [r][d_in],  dB = s dY^T U   fp32 [d_out][r]
+ * accumulate == 0 overwrites dA and dB, otherwise they are added to (one fp32
+ * addition per element).  dX may be NULL (the first layer: adapter gradients
+ * only).  U_in NULL recomputes U from X_hat.  X_codes and X_scales may be
+ * NULL when r == 0.  dA and dB carry fp32 accuracy.  T == 0: dA and dB become
+ * zero, or stay as they are when accumulating.  Other arguments, limits and
+ * errors as above and as qlora_linear_bwd.
+ */
+int qlora_fp8_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t T, int32_t r, size_t* bytes);
+int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, const uint8_t* W_scales, int64_t T,
+                         const uint8_t* X_codes, const uint8_t* X_scales, int32_t r, float alpha, const uint16_t* A,
+                         const uint16_t* B, const float* U_in, const uint16_t* dY, uint16_t* dX, float* dA, float* dB,
+                         int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The backward of an NF4 layer (qlora_linear_bwd) whose input was kept as its
+ * 8-bit form by rows:
+ *   dX = bf16( dY W_hat + s G A ),  dA = s G^T X_hat,  dB = s dY^T U
+ * U_in: as saved by the forward; NULL recomputes X_hat A^T.  dX is formed as
+ * by qlora_linear_bwd (it does not depend on X).  accumulate, T == 0, r == 0
+ * and dX == NULL as for qlora_fp8_linear_bwd.  There is no form of this call
+ * with LoRA dropout or over several layers.
+ * Errors: as qlora_linear_bwd; the workspace is 16-byte aligned.
+ */
+int qlora_checkpoint_workspace_bytes(const qlora_nf4_desc* d, int64_t T, int32_t r, size_t* bytes);
+int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, const uint8_t* codes,
+                                const float* consts, int64_t T, const uint8_t* X_codes, const uint8_t* X_scales,
+                                int32_t r, float alpha, const uint16_t* A, const uint16_t* B, const float* U_in,
+                                const uint16_t* dY, uint16_t* dX, float* dA, float* dB, int32_t accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * AdamW update of the adapter parameters ("QLoRA技术从入门到精通" §3(3):
  * after the backward pass the optimizer updates only A and B, never the
  * quantized base weight).  The arithmetic is the published AdamW method

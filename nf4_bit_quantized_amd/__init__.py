@@ -13,6 +13,7 @@ the environment variable ``QLORA_NF4_LIBRARY`` names (for example a build of
 the same sources with host-side sanitizers).
 """
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -59,6 +60,15 @@ EXPORTED = (
     "qlora_linear_bwd_multi",
     "qlora_dequantize_nf4",
     "qlora_merge_lora",
+    "qlora_fp8_sizes",
+    "qlora_quantize_fp8",
+    "qlora_dequantize_fp8",
+    "qlora_fp8_fwd_workspace_bytes",
+    "qlora_fp8_linear_fwd",
+    "qlora_fp8_bwd_workspace_bytes",
+    "qlora_fp8_linear_bwd",
+    "qlora_checkpoint_workspace_bytes",
+    "qlora_linear_bwd_checkpoint",
     "qlora_adamw_step",
     "qlora_trace_enable",
     "qlora_trace_select",
@@ -130,6 +140,17 @@ def lib() -> ctypes.CDLL:
                                            i32, vp, sz, vp]
     L.qlora_dequantize_nf4.argtypes = [dp, vp, vp, vp, vp, vp]
     L.qlora_merge_lora.argtypes = [dp, vp, vp, vp, i32, f32, vp, vp, vp, vp]
+    L.qlora_fp8_sizes.argtypes = [i64, i64, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    L.qlora_quantize_fp8.argtypes = [i64, i64, i32, vp, i32, vp, vp, vp]
+    L.qlora_dequantize_fp8.argtypes = [i64, i64, i32, vp, vp, vp, vp]
+    L.qlora_fp8_fwd_workspace_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.qlora_fp8_linear_fwd.argtypes = [i64, i64, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_fp8_bwd_workspace_bytes.argtypes = L.qlora_fp8_fwd_workspace_bytes.argtypes
+    L.qlora_fp8_linear_bwd.argtypes = [i64, i64, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz,
+                                       vp]
+    L.qlora_checkpoint_workspace_bytes.argtypes = [dp, i64, i32, ctypes.POINTER(sz)]
+    L.qlora_linear_bwd_checkpoint.argtypes = [dp, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, i32,
+                                              vp, sz, vp]
     L.qlora_adamw_step.argtypes = [ctypes.POINTER(AdamwHparams), i64, vp, vp, vp, vp, vp, vp]
     L.qlora_trace_enable.argtypes = [ctypes.c_int]
     L.qlora_trace_select.argtypes = [ctypes.c_uint32]
@@ -648,6 +669,242 @@ def qlora_merge_lora(packed, codes, consts, A, B, alpha: float, W_merged=None, s
     _check(lib().qlora_merge_lora(ctypes.byref(d), _ptr(packed), _ptr(codes), _ptr(consts), int(r), float(alpha),
                                   _ptr(A), _ptr(B), _ptr(W_merged), _stream(stream)), "qlora_merge_lora")
     return W_merged
+
+
+# ---------------------------------------------------------------------------
+# 8-bit forms: e4m3 codes with a power-of-two scale per block of 128
+# ---------------------------------------------------------------------------
+# These calls run on the device their tensors are on, whichever is current;
+# with ``stream`` given, what they allocate belongs to that stream.
+
+FP8_BLOCK = 128
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream, name: str):
+    """Make ``device`` and ``stream`` (None: the device's current one) current; yields the stream's handle."""
+    import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _one_device(name: str, *tensors):
+    """The GPU that every given tensor is on (None entries are left out)."""
+    _need_cuda(*tensors, name=name)
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"{name}: the tensors are on {len(devices)} devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _fp8_shapes(rows: int, cols: int, block_rows: int):
+    """Shapes of codes and scales."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().qlora_fp8_sizes(int(rows), int(cols), int(block_rows), ctypes.byref(a), ctypes.byref(b)),
+           "qlora_fp8_sizes")
+    ld = -(-cols // 512) * 4
+    return (rows, cols), (b.value // ld, ld)
+
+
+def qlora_fp8_sizes(rows: int, cols: int, block_rows: int = 1) -> Tuple[int, int]:
+    """(codes bytes, scales bytes) of the 8-bit form of a [rows][cols] matrix."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().qlora_fp8_sizes(int(rows), int(cols), int(block_rows), ctypes.byref(a), ctypes.byref(b)),
+           "qlora_fp8_sizes")
+    return a.value, b.value
+
+
+def _check_form(codes, scales, block_rows: int, name: str):
+    """A given 8-bit form: codes uint8 [rows][cols], scales uint8 of the rows and bytes that go with them."""
+    import torch
+    if codes is None or scales is None:
+        raise ValueError(f"{name}: codes and scales are required")
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
+        raise ValueError(f"{name}: codes must be a contiguous 2-D uint8 tensor")
+    _check_in(scales, _fp8_shapes(codes.shape[0], codes.shape[1], block_rows)[1], torch.uint8, f"{name}: scales")
+
+
+def qlora_quantize_fp8(M, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """The 8-bit form of M [rows][cols] (GPU; float32, bfloat16 or float16):
+    (codes uint8 [rows][cols], scales uint8 [ceil(rows / block_rows)][4 ceil(cols / 512)]).
+    block_rows 1: a scale per row and 128 columns (a layer's input, kept for its backward or multiplied);
+    128: a scale per 128 x 128 block (a weight).  ``codes.view(torch.float8_e4m3fn)`` are the codes' values,
+    ``scales.view(torch.float8_e8m0fnu)`` the scales'."""
+    import torch
+    fmts = {torch.float32: QLORA_W_F32, torch.bfloat16: QLORA_W_BF16, torch.float16: QLORA_W_F16}
+    _matrix(M, "M")
+    if M.dtype not in fmts:
+        raise ValueError("M must be a float32, bfloat16 or float16 tensor")
+    if not M.is_contiguous():
+        raise ValueError("M must be contiguous")
+    shape_c, shape_s = _fp8_shapes(M.shape[0], M.shape[1], block_rows)
+    _check_out(codes, shape_c, torch.uint8, "codes")
+    _check_out(scales, shape_s, torch.uint8, "scales")
+    device = _one_device("qlora_quantize_fp8", M, codes, scales)
+    with _launch_on(device, stream, "qlora_quantize_fp8") as st:
+        if codes is None:
+            codes = torch.empty(shape_c, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.empty(shape_s, dtype=torch.uint8, device=device)
+        _check(lib().qlora_quantize_fp8(M.shape[0], M.shape[1], int(block_rows), _ptr(M), fmts[M.dtype], _ptr(codes),
+                                        _ptr(scales), st), "qlora_quantize_fp8")
+    return codes, scales
+
+
+def qlora_dequantize_fp8(codes, scales, block_rows: int = 1, M_hat=None, stream=None):
+    """The bf16 matrix that an 8-bit form stands for."""
+    import torch
+    _check_form(codes, scales, block_rows, "qlora_dequantize_fp8")
+    _check_out(M_hat, codes.shape, torch.bfloat16, "M_hat")
+    device = _one_device("qlora_dequantize_fp8", codes, scales, M_hat)
+    with _launch_on(device, stream, "qlora_dequantize_fp8") as st:
+        if M_hat is None:
+            M_hat = torch.empty(tuple(codes.shape), dtype=torch.bfloat16, device=device)
+        _check(lib().qlora_dequantize_fp8(codes.shape[0], codes.shape[1], int(block_rows), _ptr(codes), _ptr(scales),
+                                          _ptr(M_hat), st), "qlora_dequantize_fp8")
+    return M_hat
+
+
+def qlora_fp8_fwd_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_fp8_fwd_workspace_bytes(int(d_out), int(d_in), int(T), int(r), ctypes.byref(n)),
+           "qlora_fp8_fwd_workspace_bytes")
+    return n.value
+
+
+def qlora_fp8_bwd_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_fp8_bwd_workspace_bytes(int(d_out), int(d_in), int(T), int(r), ctypes.byref(n)),
+           "qlora_fp8_bwd_workspace_bytes")
+    return n.value
+
+
+def qlora_fp8_linear_fwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: float, Y=None, U_out=None,
+                         want_u: bool = True, workspace=None, stream=None):
+    """Forward of a layer on an 8-bit weight (block_rows 128) for an input in the 8-bit form by rows:
+    returns (Y bf16 [T][d_out], U fp32 [T][r] or None).  A, B may be None (r = 0)."""
+    import torch
+    name = "qlora_fp8_linear_fwd"
+    _check_form(W_codes, W_scales, FP8_BLOCK, f"{name}: W")
+    _check_form(X_codes, X_scales, 1, f"{name}: X")
+    d_out, d_in = W_codes.shape
+    T = X_codes.shape[0]
+    r = 0 if A is None else A.shape[0]
+    if X_codes.shape[1] != d_in:
+        raise ValueError(f"{name}: X has {X_codes.shape[1]} columns, the weight {d_in}")
+    _check_adapter(A, B, d_out, d_in, r)
+    _check_out(Y, (T, d_out), torch.bfloat16, "Y")
+    _check_out(U_out, (T, r), torch.float32, "U_out")
+    device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, Y, U_out, workspace)
+    nbytes = qlora_fp8_fwd_workspace_bytes(d_out, d_in, T, r)
+    with _launch_on(device, stream, name) as st:
+        if Y is None:
+            Y = torch.empty((T, d_out), dtype=torch.bfloat16, device=device)
+        if U_out is None and want_u and r > 0:
+            U_out = torch.empty((T, r), dtype=torch.float32, device=device)
+        ws = _workspace(nbytes, device, workspace)
+        _check(lib().qlora_fp8_linear_fwd(d_out, d_in, _ptr(W_codes), _ptr(W_scales), T, _ptr(X_codes), _ptr(X_scales),
+                                          r, float(alpha), _ptr(A), _ptr(B), _ptr(Y), _ptr(U_out), _ptr(ws), nbytes,
+                                          st), name)
+    return Y, U_out
+
+
+def _grad_buffers(dX, dA, dB, T: int, d_out: int, d_in: int, r: int, accumulate: bool):
+    """The given gradient outputs of a backward from a checkpoint, checked."""
+    import torch
+    _check_out(dX, (T, d_in), torch.bfloat16, "dX")
+    if r == 0:
+        return
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate=True needs the dA and dB to add to")
+    _check_out(dA, (r, d_in), torch.float32, "dA")
+    _check_out(dB, (d_out, r), torch.float32, "dB")
+
+
+def qlora_fp8_linear_bwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: float, dY, U_in=None, dX=None, dA=None,
+                         dB=None, want_dx: bool = True, workspace=None, stream=None, accumulate: bool = False):
+    """Backward of qlora_fp8_linear_fwd: returns (dX bf16 [T][d_in] or None, dA fp32 [r][d_in], dB fp32
+    [d_out][r]); dX from the 8-bit form of dY.  accumulate=True adds to the given dA and dB."""
+    import torch
+    name = "qlora_fp8_linear_bwd"
+    _check_form(W_codes, W_scales, FP8_BLOCK, f"{name}: W")
+    _check_form(X_codes, X_scales, 1, f"{name}: X")
+    d_out, d_in = W_codes.shape
+    T = X_codes.shape[0]
+    r = 0 if A is None else A.shape[0]
+    if X_codes.shape[1] != d_in:
+        raise ValueError(f"{name}: X has {X_codes.shape[1]} columns, the weight {d_in}")
+    _check_adapter(A, B, d_out, d_in, r)
+    _check_in(dY, (T, d_out), torch.bfloat16, "dY")
+    _check_out(U_in, (T, r), torch.float32, "U_in")
+    _grad_buffers(dX, dA, dB, T, d_out, d_in, r, accumulate)
+    device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, dY, U_in, dX, dA, dB, workspace)
+    nbytes = qlora_fp8_bwd_workspace_bytes(d_out, d_in, T, r)
+    with _launch_on(device, stream, name) as st:
+        if dX is None and want_dx:
+            dX = torch.empty((T, d_in), dtype=torch.bfloat16, device=device)
+        if r > 0 and dA is None:
+            dA = torch.empty((r, d_in), dtype=torch.float32, device=device)
+        if r > 0 and dB is None:
+            dB = torch.empty((d_out, r), dtype=torch.float32, device=device)
+        ws = _workspace(nbytes, device, workspace)
+        _check(lib().qlora_fp8_linear_bwd(d_out, d_in, _ptr(W_codes), _ptr(W_scales), T, _ptr(X_codes), _ptr(X_scales),
+                                          r, float(alpha), _ptr(A), _ptr(B), _ptr(U_in), _ptr(dY), _ptr(dX), _ptr(dA),
+                                          _ptr(dB), 1 if accumulate else 0, _ptr(ws), nbytes, st), name)
+    return dX, dA, dB
+
+
+def qlora_linear_bwd_checkpoint(packed, codes, consts, X_codes, X_scales, A, B, alpha: float, dY, U_in=None, dX=None,
+                                dA=None, dB=None, want_dx: bool = True, workspace=None, stream=None,
+                                table: int = TABLE_NF4, accumulate: bool = False):
+    """qlora_linear_bwd for a layer whose input was kept in the 8-bit form by rows (qlora_quantize_fp8):
+    returns (dX, dA, dB), dA being the gradient over the values the form stands for."""
+    import torch
+    name = "qlora_linear_bwd_checkpoint"
+    _check_weight(packed, codes, consts)
+    _check_form(X_codes, X_scales, 1, f"{name}: X")
+    d_out, d_in = packed.shape[0], packed.shape[1] * 2
+    T = X_codes.shape[0]
+    r = 0 if A is None else A.shape[0]
+    if X_codes.shape[1] != d_in:
+        raise ValueError(f"{name}: X has {X_codes.shape[1]} columns, the weight {d_in}")
+    _check_adapter(A, B, d_out, d_in, r)
+    _check_in(dY, (T, d_out), torch.bfloat16, "dY")
+    _check_out(U_in, (T, r), torch.float32, "U_in")
+    _grad_buffers(dX, dA, dB, T, d_out, d_in, r, accumulate)
+    device = _one_device(name, packed, codes, consts, X_codes, X_scales, A, B, dY, U_in, dX, dA, dB, workspace)
+    d = _stored_desc(packed, codes, consts, table)
+    n = ctypes.c_size_t()
+    _check(lib().qlora_checkpoint_workspace_bytes(ctypes.byref(d), T, r, ctypes.byref(n)),
+           "qlora_checkpoint_workspace_bytes")
+    with _launch_on(device, stream, name) as st:
+        if dX is None and want_dx:
+            dX = torch.empty((T, d_in), dtype=torch.bfloat16, device=device)
+        if r > 0 and dA is None:
+            dA = torch.empty((r, d_in), dtype=torch.float32, device=device)
+        if r > 0 and dB is None:
+            dB = torch.empty((d_out, r), dtype=torch.float32, device=device)
+        ws = _workspace(n.value, device, workspace)
+        _check(lib().qlora_linear_bwd_checkpoint(ctypes.byref(d), _ptr(packed), _ptr(codes), _ptr(consts), T,
+                                                 _ptr(X_codes), _ptr(X_scales), r, float(alpha), _ptr(A), _ptr(B),
+                                                 _ptr(U_in), _ptr(dY), _ptr(dX), _ptr(dA), _ptr(dB),
+                                                 1 if accumulate else 0, _ptr(ws), n.value, st), name)
+    return dX, dA, dB
+
+
+def qlora_checkpoint_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+    """Workspace of qlora_linear_bwd_checkpoint (blocks of 64, double quantization)."""
+    d = _desc(d_out, d_in)
+    n = ctypes.c_size_t()
+    _check(lib().qlora_checkpoint_workspace_bytes(ctypes.byref(d), int(T), int(r), ctypes.byref(n)),
+           "qlora_checkpoint_workspace_bytes")
+    return n.value
 
 
 # ---------------------------------------------------------------------------

@@ -6,6 +6,8 @@
 #include <cstring>
 #include <mutex>
 
+#include "api.hpp"
+#include "fp8.hpp"
 #include "fused.hpp"
 #include "lora_stream.hpp"
 #include <cmath>
@@ -15,12 +17,10 @@
 #include "dropout.hpp"
 #include "skinny.hpp"
 #include "trace.hpp"
-#include "../../include/qlora.h"
 
 namespace qlora {
 hipError_t launch_nf4_quantize(const void* W, int wformat, uint8_t* packed, uint8_t* codes, float* consts,
                                int64_t numel, int blocksize, int dq, int table, hipStream_t stream);
-hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t stream);
 hipError_t launch_export(const uint8_t* packed, const uint8_t* codes, const float* consts, int64_t N, int64_t K,
                          int r, float s, const uint16_t* A, const uint16_t* B, uint16_t* W, int table,
                          int bshift, int dq, hipStream_t stream);
@@ -31,11 +31,6 @@ using namespace qlora;
 namespace {
 
 constexpr int64_t kDecodeMaxT = 16;
-constexpr int kMaxRank = 128;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // log2(blocksize / 64): 64-weight chunk index -> block index
 int block_shift(const qlora_nf4_desc* d) { return d->blocksize == 256 ? 2 : (d->blocksize == 128 ? 1 : 0); }
@@ -57,14 +52,6 @@ int check_desc(const qlora_nf4_desc* d) {
   return QLORA_OK;
 }
 
-int64_t hilo_ld(int32_t r) { return cdiv(2 * (int64_t)r, 64) * 64; }
-
-// The kernels address every dense operand with 32-bit byte offsets (buffer
-// resources capped below 2 GiB): the packed weight, X, Y, dY, dX and the
-// workspace's [T][2r] pairs must each stay below kMaxOperandBytes.
-constexpr int64_t kMaxOperandBytes = 0x7FFFFFF0LL;
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
-
 int check_layer(const qlora_nf4_desc* d, int64_t T, int32_t r) {
   const int st = check_desc(d);
   if (st) return st;
@@ -76,18 +63,6 @@ int check_layer(const qlora_nf4_desc* d, int64_t T, int32_t r) {
     return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
-
-// Workspace carving: a bump allocator over the caller's buffer.
-struct Carve {
-  char* base;
-  size_t off = 0;
-  explicit Carve(void* b) : base(static_cast<char*>(b)) {}
-  void* take(size_t bytes) {
-    void* p = base ? base + off : nullptr;
-    off += align256(bytes);
-    return p;
-  }
-};
 
 // Scratch for the split-contraction partials of one rank-r product.
 size_t skinny_part_bytes(int64_t mrows, int64_t clen, int64_t cols) {
@@ -178,11 +153,6 @@ void skinny_q(SkinnyParams& S, const uint16_t* Q, int64_t ldq, int64_t qrows, in
   S.Q = Q; S.ldq = ldq; S.qrows = qrows; S.q_mode = q_mode; S.qvec = vec_ok(Q, ldq);
 }
 
-#define HIP_TRY(expr)                          \
-  do {                                         \
-    if ((expr) != hipSuccess) return QLORA_ERR_HIP; \
-  } while (0)
-
 // U = X A^T (fp32 into U), and the hi/lo bf16 pair of s*U into Us.
 int lora_down(const uint16_t* X, const uint16_t* A, int64_t T, int64_t K, int32_t r, float s, float* part,
               float* U, uint16_t* Us, hipStream_t st) {
@@ -207,6 +177,29 @@ int lora_down(const uint16_t* X, const uint16_t* A, int64_t T, int64_t K, int32_
 }
 
 }  // namespace
+
+namespace qlora {
+size_t lora_g_part_bytes(int64_t T, int64_t N, int32_t r) {
+  return lora_rows_ok(T, r) ? lora_rows_part_bytes(T, N, r) : skinny_part_bytes(T, N, r);
+}
+
+int lora_g(const uint16_t* dY, const uint16_t* B, int64_t T, int64_t N, int32_t r, float s, float* part,
+           size_t part_bytes, float* G, uint16_t* Gs, hipStream_t st) {
+  if (lora_rows_ok(T, r)) {
+    RowsParams R{};
+    R.P = dY; R.ldp = N; R.M = T; R.D = N;
+    R.Q = B; R.ldq = r; R.q_strided = 1; R.r = r; R.s = s;
+    R.Vout = G; R.Hout = Gs; R.ldh = hilo_ld(r);
+    HIP_TRY(launch_lora_rows(R, part, part_bytes, st, KID_LORA_G));
+    return QLORA_OK;
+  }
+  SkinnyParams S = skinny(dY, N, true, T, N, r, s, r, OUT_ROWS_HILO, part);
+  skinny_q(S, B, r, r, Q_STRIDED);
+  S.Vout = G; S.Hout = Gs; S.ldh = hilo_ld(r);
+  HIP_TRY(launch_skinny(S, st, KID_LORA_G));
+  return QLORA_OK;
+}
+}  // namespace qlora
 
 extern "C" {
 
@@ -821,6 +814,92 @@ int qlora_linear_bwd_dropout(const qlora_nf4_desc* d, const uint8_t* packed, con
   HIP_TRY(launch_dropout_input(X, keep, c, T, d->d_in, Xd, (hipStream_t)stream));
   return enqueue_bwd(d, packed, codes, consts, T, X, Xd, keep, c, r, alpha, A, B, U_in, dY, dX, dA, dB,
                      ws_at(workspace, xd), stream, accumulate != 0, 0);
+}
+
+namespace {
+// The backward whose X is an 8-bit checkpoint: the plain backward's workspace
+// (its pair of s*G feeds the dX product), then G and U in fp32 and the partial
+// sums of U and of the adapter's gradients, which never live at the same time.
+struct CheckpointWs {
+  void* bwd = nullptr;
+  float* G = nullptr;
+  float* U = nullptr;
+  float* part = nullptr;
+  size_t part_bytes = 0;
+  size_t bytes = 0;
+};
+
+static CheckpointWs plan_checkpoint(const qlora_nf4_desc* d, int64_t T, int32_t r, void* ws) {
+  CheckpointWs w;
+  Carve c(ws);
+  if (r > 0 && T > 0) {
+    w.bwd = c.take(plan_bwd(d, T, r, nullptr).bytes);
+    w.G = static_cast<float*>(c.take((size_t)T * r * 4));
+    w.U = static_cast<float*>(c.take((size_t)T * r * 4));
+    w.part_bytes = std::max(std::max(fp8_down_part_bytes(T, d->d_in, r), lora_g_part_bytes(T, d->d_out, r)),
+                            fp8_grad_part_bytes(T, d->d_in, d->d_out, r));
+    w.part = static_cast<float*>(c.take(w.part_bytes));
+  }
+  w.bytes = c.off;
+  return w;
+}
+}  // namespace
+
+int qlora_checkpoint_workspace_bytes(const qlora_nf4_desc* d, int64_t T, int32_t r, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_NULL;
+  const int st = check_layer(d, T, r);
+  if (st) return st;
+  *bytes = plan_checkpoint(d, T, r, nullptr).bytes;
+  return QLORA_OK;
+}
+
+int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, const uint8_t* codes,
+                                const float* consts, int64_t T, const uint8_t* X_codes, const uint8_t* X_scales,
+                                int32_t r, float alpha, const uint16_t* A, const uint16_t* B, const float* U_in,
+                                const uint16_t* dY, uint16_t* dX, float* dA, float* dB, int32_t accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_layer(d, T, r);
+  if (st) return st;
+  if (!packed || (!codes && d->dq_blocksize) || !consts) return QLORA_ERR_NULL;
+  if (T > 0 && (!dY || (r > 0 && (!X_codes || !X_scales)))) return QLORA_ERR_NULL;
+  if (r > 0 && (!A || !B || !dA || !dB)) return QLORA_ERR_NULL;
+  if (!aligned16(packed) || !aligned16(X_codes) || !aligned4(X_scales) || !aligned16(dY) || !aligned16(A) ||
+      !aligned16(B) || !aligned16(dX) || !aligned16(U_in) || !aligned16(dA) || !aligned16(dB))
+    return QLORA_ERR_UNSUPPORTED;
+  const size_t need = plan_checkpoint(d, T, r, nullptr).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return QLORA_ERR_UNSUPPORTED;
+  hipStream_t s_ = (hipStream_t)stream;
+  const int64_t N = d->d_out, K = d->d_in;
+  if (T == 0) {
+    if (r > 0 && !accumulate) {
+      HIP_TRY(launch_fill_zero(dA, (int64_t)r * K, s_));
+      HIP_TRY(launch_fill_zero(dB, N * r, s_));
+    }
+    return QLORA_OK;
+  }
+  const CheckpointWs w = plan_checkpoint(d, T, r, workspace);
+  const float s = r > 0 ? alpha / (float)r : 0.0f;
+  const float* U = U_in;
+  if (r > 0) {
+    if (!U) {
+      const Fp8DownParams Dn{X_codes, X_scales, A, T, K, r, s, w.U, nullptr, hilo_ld(r), w.part, w.part_bytes};
+      HIP_TRY(launch_fp8_down(Dn, s_));
+      U = w.U;
+    }
+    const int e = lora_g(dY, B, T, N, r, s, w.part, w.part_bytes, w.G, plan_bwd(d, T, r, w.bwd).Gs, s_);
+    if (e) return e;
+  }
+  if (dX) {
+    const int e = enqueue_bwd(d, packed, codes, consts, T, nullptr, nullptr, nullptr, 1.0f, r, alpha, A, B, U, dY, dX,
+                              dA, dB, w.bwd, stream, accumulate, 0, kBwdDx);
+    if (e) return e;
+  }
+  if (r > 0) {
+    const Fp8GradParams Gr{X_codes, X_scales, dY, w.G, U, T, K, N, r, s, dA, dB, accumulate != 0, w.part, w.part_bytes};
+    HIP_TRY(launch_fp8_grad(Gr, s_));
+  }
+  return QLORA_OK;
 }
 
 int qlora_adamw_step(const qlora_adamw_hparams* h, int64_t n, float* param, const float* grad, float* exp_avg,

@@ -1,0 +1,454 @@
+// The adapter's products over the 8-bit form of the layer's input (fp8.hip):
+//   down:  U[t][j] = sum_k X[t][k] A[j][k]
+//   grad:  dA[j][k] = s sum_t G[t][j] X[t][k],  dB[n][j] = s sum_t dY[t][n] U[t][j]
+// Every e4m3 code times its power-of-two scale is a bf16 value, so X is
+// restored exactly in registers and enters v_mfma_f32_16x16x32_bf16; sums are
+// fp32.  G and U are fp32; for the gradients each is split into three bf16
+// terms (hi + mid + lo carry all 24 bits), so the gradients keep fp32
+// accuracy, where a pair of terms would round them to about 17 bits.
+#include "dma.hpp"
+#include "fp8.hpp"
+#include "lds_tr.hpp"
+#include "trace.hpp"
+
+namespace qlora {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+using ldstr::tr_frag_swz;
+using ldstr::tr_swz;
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+// Eight codes (two dwords) restored: exact, save below bf16's own range.
+__device__ __forceinline__ u32x4_t restore8(uint32_t a, uint32_t b, float k) {
+  return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, k, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, k, true))};
+}
+
+// ---------------------------------------------------------------------------
+// down
+//
+// A workgroup owns 16 RT tokens and 16 JT columns of U for one range of the
+// contraction; its NW waves take the range's chunks of 128 in turn and add
+// their tiles in LDS in wave order.  Fragments come straight from global
+// memory: lane l of token row l % 16 takes the 32 codes 32 (l/16) .. +31 of
+// the chunk, which are its share of four MFMAs.
+// ---------------------------------------------------------------------------
+struct DownLaunch {
+  Fp8DownParams p;
+  int32_t ttiles, jtiles, nsplit;
+  int32_t chunks, chunks_per_split;
+};
+
+// Column c < ldh of row t of Us and, for c < r, of U, from the sums v(j).
+template <typename SumJ>
+__device__ __forceinline__ void down_out(const Fp8DownParams& p, int64_t t, int c, SumJ v_of) {
+  uint16_t h = 0;
+  if (c < 2 * p.r) {
+    const float v = v_of(c < p.r ? c : c - p.r);
+    if (p.U && c < p.r) p.U[t * p.r + c] = v;
+    uint16_t hi, lo;
+    split_bf16(p.s * v, hi, lo);
+    h = c < p.r ? hi : lo;
+  }
+  if (p.Us) p.Us[t * p.ldh + c] = h;
+}
+
+template <int RT, int JT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_fp8_down(DownLaunch L) {
+  constexpr int TOK = 16 * RT, COL = 16 * JT, LD = COL + 1;
+  __shared__ float red[NW][TOK][LD];
+  const Fp8DownParams& p = L.p;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = lane & 15, g = lane >> 4;
+  int b = (int)blockIdx.x;
+  const int split = b / (L.ttiles * L.jtiles);
+  b -= split * (L.ttiles * L.jtiles);
+  const int64_t t0 = (int64_t)(b / L.jtiles) * TOK;
+  const int j0 = (b % L.jtiles) * COL;
+  const int64_t ldx = fp8_scale_ld(p.K);
+  const int c_begin = split * L.chunks_per_split;
+  const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
+
+  f32x4_t acc[RT][JT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  // rows past the end repeat the last one; their sums are never stored
+  const uint8_t* xrow[RT];
+  const uint8_t* srow[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int64_t t = t0 + 16 * rt + i < p.T ? t0 + 16 * rt + i : p.T - 1;
+    xrow[rt] = p.X + t * p.K;
+    srow[rt] = p.Xs + t * ldx;
+  }
+  const uint16_t* arow[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) {
+    const int j = j0 + 16 * jt + i < p.r ? j0 + 16 * jt + i : p.r - 1;
+    arow[jt] = p.A + (int64_t)j * p.K;
+  }
+  for (int ch = c_begin + wave; ch < c_end; ch += NW) {
+    const int64_t k = (int64_t)ch * 128 + 32 * g;
+    const bool in = k < p.K;  // the last chunk of a row may be half a chunk
+    u32x4_t x[RT][2];
+    float sc[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      sc[rt] = scale_of(srow[rt][ch]);
+      const u32x4_t* src = reinterpret_cast<const u32x4_t*>(xrow[rt] + (in ? k : 0));
+      x[rt][0] = src[0];
+      x[rt][1] = src[1];
+      if (!in) x[rt][0] = x[rt][1] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const u32x4_t* src = reinterpret_cast<const u32x4_t*>(arow[jt] + (in ? k : 0));
+      u32x4_t a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[q] = in ? src[q] : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const u32x4_t v = restore8(x[rt][q >> 1][2 * (q & 1)], x[rt][q >> 1][2 * (q & 1) + 1], sc[rt]);
+          acc[rt][jt] = mfma16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, a[q]), acc[rt][jt]);
+        }
+    }
+  }
+  // lane l, value v: token 16 rt + 4 (l/16) + v, column 16 jt + l % 16
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[wave][16 * rt + 4 * g + v][16 * jt + i] = acc[rt][jt][v];
+  __syncthreads();
+  auto sum = [&](int rr, int j) {
+    float v = red[0][rr][j];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[w][rr][j];
+    return v;
+  };
+  if (L.nsplit > 1) {
+    float* part = p.part + (int64_t)split * p.T * p.r;
+    for (int e = threadIdx.x; e < TOK * COL; e += NW * 64) {
+      const int rr = e / COL, j = e % COL;
+      if (t0 + rr < p.T && j0 + j < p.r) part[(t0 + rr) * p.r + j0 + j] = sum(rr, j);
+    }
+    return;
+  }
+  // this workgroup's columns of U, their hi and lo columns of Us, and (its
+  // share of) the padding
+  for (int e = threadIdx.x; e < TOK * COL; e += NW * 64) {
+    const int rr = e / COL, j = j0 + e % COL;
+    const int64_t t = t0 + rr;
+    if (t >= p.T) continue;
+    if (j < p.r) {
+      const float v = sum(rr, j - j0);
+      if (p.U) p.U[t * p.r + j] = v;
+      if (p.Us) {
+        uint16_t hi, lo;
+        split_bf16(p.s * v, hi, lo);
+        p.Us[t * p.ldh + j] = hi;
+        p.Us[t * p.ldh + p.r + j] = lo;
+      }
+    }
+    if (p.Us)
+      for (int64_t c = 2 * p.r + j; c < p.ldh; c += COL * L.jtiles) p.Us[t * p.ldh + c] = 0;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_fp8_down_sum(DownLaunch L) {
+  const Fp8DownParams& p = L.p;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= p.T * p.ldh) return;
+  const int64_t t = e / p.ldh;
+  down_out(p, t, (int)(e - t * p.ldh), [&](int j) {
+    float v = p.part[t * p.r + j];
+    for (int q = 1; q < L.nsplit; ++q) v += p.part[((int64_t)q * p.T + t) * p.r + j];
+    return v;
+  });
+}
+
+// many tokens: 64 x r tiles, the contraction split until the workgroups fill
+// the CUs; fewer: 16 x 16 tiles over the whole contraction, in one launch
+constexpr int64_t kDownManyT = 512;
+int down_rt(int r) { return r <= 64 ? 4 : 2; }
+int down_splits(int64_t T, int64_t K, int r) {
+  if (T < kDownManyT) return 1;
+  const int64_t tiles = (T + 16 * down_rt(r) - 1) / (16 * down_rt(r)), chunks = (K + 127) / 128;
+  int64_t s = 256 / tiles;
+  if (s > chunks / 8) s = chunks / 8;
+  return (int)(s < 1 ? 1 : s);
+}
+
+// ---------------------------------------------------------------------------
+// grad: out[m][j] = s sum_t P[t][m] Q[t][j]
+//
+// A workgroup of eight waves owns 256 columns m of P (wave w: 32 of them) and
+// every j for one range of tokens, in chunks of 32 tokens: P's tile goes
+// through registers (restored, if it is codes) into LDS as bf16 [32][256], Q's
+// as three planes of bf16 [32][16 JT].  Both operands are read back with
+// transposing reads, the contraction running down the rows.
+// ---------------------------------------------------------------------------
+constexpr int kGradM = 256;
+constexpr int kGradChunk = 32;
+
+struct GradLaunch {
+  Fp8GradParams p;
+  int32_t slabs_a, slabs_b;  // of dA's columns (K) and of dB's rows (N)
+  int32_t nsplit, chunks, chunks_per_split;
+};
+
+template <int JT>
+__global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
+  constexpr int QLD = 16 * JT;
+  constexpr int kP = kGradChunk * kGradM, kQ = kGradChunk * QLD;  // elements
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][kP + 3 * kQ];
+  const Fp8GradParams& p = L.p;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = lane & 15, g = lane >> 4;
+  const int slabs = L.slabs_a + L.slabs_b;
+  const int split = (int)blockIdx.x / slabs;
+  int slab = (int)blockIdx.x - split * slabs;
+  const bool second = slab >= L.slabs_a;  // dB
+  if (second) slab -= L.slabs_a;
+  const int64_t m0 = (int64_t)slab * kGradM;
+  const int64_t D = second ? p.N : p.K;
+  const float* Q = second ? p.U : p.G;
+  const int r = p.r;
+  const int64_t ldx = fp8_scale_ld(p.K);
+  const int c_begin = split * L.chunks_per_split;
+  const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
+
+  // thread: row tid / 16 of the chunk, 16 columns of P and JT of Q
+  const int row = threadIdx.x >> 4, pc = threadIdx.x & 15;
+  const int64_t col = m0 + 16 * pc;
+  u32x4_t pw[2];
+  uint32_t ps = 127;
+  float qv[JT];
+  auto fetch = [&](int ch) {
+    const int64_t t = (int64_t)ch * kGradChunk + row;
+    const bool in = t < p.T && col < D;
+    pw[0] = pw[1] = u32x4_t{0u, 0u, 0u, 0u};
+    if (in) {
+      if (second) {
+        const u32x4_t* src = reinterpret_cast<const u32x4_t*>(p.dY + t * p.N + col);
+        pw[0] = src[0];
+        pw[1] = src[1];
+      } else {
+        pw[0] = *reinterpret_cast<const u32x4_t*>(p.X + t * p.K + col);
+        ps = p.Xs[t * ldx + (col >> 7)];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < JT; ++q) {
+      const int j = pc + 16 * q;
+      qv[q] = t < p.T && j < r ? Q[t * r + j] : 0.0f;
+    }
+  };
+  auto stage = [&](int buf) {
+    uint16_t* P = lds[buf];
+    u32x4_t a = pw[0], b = pw[1];
+    if (!second) {
+      const float k = scale_of(ps);
+      b = restore8(pw[0][2], pw[0][3], k);
+      a = restore8(pw[0][0], pw[0][1], k);
+    }
+    const int s = tr_swz(row, kGradM / 8);
+    *reinterpret_cast<u32x4_t*>(P + row * kGradM + (((2 * pc) ^ s) << 3)) = a;
+    *reinterpret_cast<u32x4_t*>(P + row * kGradM + (((2 * pc + 1) ^ s) << 3)) = b;
+    const int sq = tr_swz(row, QLD / 8);
+#pragma unroll
+    for (int q = 0; q < JT; ++q) {
+      const int j = pc + 16 * q;
+      const float v = p.s * qv[q];
+      uint16_t h, m, l;
+      split_bf16(v, h, m);
+      const float rest = v - bf16_bits_to_f32(h);
+      l = f32_to_bf16_bits(rest - bf16_bits_to_f32(m));
+      uint16_t* dst = P + kP + row * QLD + ((((j >> 3) ^ sq) << 3) | (j & 7));
+      dst[0] = h;
+      dst[kQ] = m;
+      dst[2 * kQ] = l;
+    }
+  };
+
+  f32x4_t acc[2][JT];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) acc[a][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  if (c_begin < c_end) fetch(c_begin);
+  for (int ch = c_begin; ch < c_end; ++ch) {
+    const int buf = (ch - c_begin) & 1;
+    stage(buf);
+    if (ch + 1 < c_end) fetch(ch + 1);
+    lds_barrier();  // the chunk is staged; every wave is done with the other buffer
+    const uint16_t* P = lds[buf];
+    bf16x8_t pa[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) pa[a] = tr_frag_swz(P, kGradM, 8 * g, 32 * wave + 16 * a);
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+      for (int q = 2; q >= 0; --q) {  // the smallest terms first
+        const bf16x8_t qb = tr_frag_swz(P + kP + q * kQ, QLD, 8 * g, 16 * jt);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) acc[a][jt] = mfma16(pa[a], qb, acc[a][jt]);
+      }
+  }
+
+  // lane l, value v: column m = 32 wave + 16 a + 4 (l/16) + v, j = 16 jt + l % 16
+  const bool split_out = L.nsplit > 1;
+  float* out = second ? p.dB : p.dA;
+  if (split_out) out = p.part + (int64_t)split * r * (p.K + p.N) + (second ? (int64_t)r * p.K : 0);
+  const bool add = !split_out && p.accumulate;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const int64_t m = m0 + 32 * wave + 16 * a + 4 * g;
+    if (m >= D) continue;
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const int j = 16 * jt + i;
+      if (j >= r) continue;
+      if (second) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float* dst = out + (m + v) * r + j;
+          *dst = add ? *dst + acc[a][jt][v] : acc[a][jt][v];
+        }
+      } else {
+        f32x4_t* dst = reinterpret_cast<f32x4_t*>(out + (int64_t)j * D + m);
+        f32x4_t o = acc[a][jt];
+        if (add) {
+          const f32x4_t w = *dst;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = w[v] + o[v];
+        }
+        *dst = o;
+      }
+    }
+  }
+}
+
+// The token ranges' partial sums in order (dA's, then dB's), four elements a
+// thread; K and N are multiples of 64, so no piece straddles the two.
+__global__ __launch_bounds__(256) void k_fp8_grad_sum(GradLaunch L) {
+  const Fp8GradParams& p = L.p;
+  const int64_t na = (int64_t)p.r * p.K, n = na + (int64_t)p.r * p.N;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= n) return;
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(p.part + e);
+  for (int q = 1; q < L.nsplit; ++q) {
+    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(p.part + q * n + e);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] += w[x];
+  }
+  f32x4_t* dst = reinterpret_cast<f32x4_t*>(e < na ? p.dA + e : p.dB + (e - na));
+  if (p.accumulate) {
+    const f32x4_t o = *dst;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = o[x] + v[x];
+  }
+  *dst = v;
+}
+
+int grad_splits(int64_t T, int64_t K, int64_t N) {
+  const int64_t slabs = (K + kGradM - 1) / kGradM + (N + kGradM - 1) / kGradM;
+  const int64_t chunks = (T + kGradChunk - 1) / kGradChunk;
+  int64_t s = 512 / slabs;
+  if (s > chunks / 4) s = chunks / 4;
+  if (s > 16) s = 16;
+  return (int)(s < 1 ? 1 : s);
+}
+
+}  // namespace
+
+size_t fp8_down_part_bytes(int64_t T, int64_t K, int r) {
+  const int s = down_splits(T, K, r);
+  return s > 1 ? (size_t)s * T * r * 4 : 0;
+}
+
+hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream) {
+  DownLaunch L{};
+  L.p = p;
+  L.chunks = (int32_t)((p.K + 127) / 128);
+  L.nsplit = down_splits(p.T, p.K, p.r);
+  L.chunks_per_split = (L.chunks + L.nsplit - 1) / L.nsplit;
+  if (L.nsplit > 1 && (!p.part || p.part_bytes < fp8_down_part_bytes(p.T, p.K, p.r))) return hipErrorInvalidValue;
+  const int jt = (p.r + 15) / 16;
+  {
+    KernelEvents ev(KID_FP8_DOWN);
+    const hipEvent_t e0 = ev.start(), e1 = ev.stop();
+    if (p.T < kDownManyT) {
+      L.ttiles = (int32_t)((p.T + 15) / 16);
+      L.jtiles = jt;
+      hipExtLaunchKernelGGL((k_fp8_down<1, 1, 16>), dim3((unsigned)(L.ttiles * L.jtiles)), dim3(1024), 0, stream, e0, e1, 0, L);
+    } else {
+      const int tok = 16 * down_rt(p.r);
+      L.ttiles = (int32_t)((p.T + tok - 1) / tok);
+      L.jtiles = 1;
+      const dim3 grid((unsigned)(L.ttiles * L.nsplit)), block(512);
+      if (jt == 1) hipExtLaunchKernelGGL((k_fp8_down<4, 1, 8>), grid, block, 0, stream, e0, e1, 0, L);
+      else if (jt == 2) hipExtLaunchKernelGGL((k_fp8_down<4, 2, 8>), grid, block, 0, stream, e0, e1, 0, L);
+      else if (jt <= 4) hipExtLaunchKernelGGL((k_fp8_down<4, 4, 8>), grid, block, 0, stream, e0, e1, 0, L);
+      else hipExtLaunchKernelGGL((k_fp8_down<2, 8, 8>), grid, block, 0, stream, e0, e1, 0, L);
+    }
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || L.nsplit == 1) return e;
+  KernelEvents ev(KID_REDUCE);
+  hipExtLaunchKernelGGL(k_fp8_down_sum, dim3((unsigned)((p.T * p.ldh + 255) / 256)), dim3(256), 0, stream, ev.start(),
+                        ev.stop(), 0, L);
+  return hipGetLastError();
+}
+
+size_t fp8_grad_part_bytes(int64_t T, int64_t K, int64_t N, int r) {
+  const int s = grad_splits(T, K, N);
+  return s > 1 ? (size_t)s * r * (K + N) * 4 : 0;
+}
+
+hipError_t launch_fp8_grad(const Fp8GradParams& p, hipStream_t stream) {
+  GradLaunch L{};
+  L.p = p;
+  L.slabs_a = (int32_t)((p.K + kGradM - 1) / kGradM);
+  L.slabs_b = (int32_t)((p.N + kGradM - 1) / kGradM);
+  L.chunks = (int32_t)((p.T + kGradChunk - 1) / kGradChunk);
+  L.nsplit = grad_splits(p.T, p.K, p.N);
+  L.chunks_per_split = (L.chunks + L.nsplit - 1) / L.nsplit;
+  if (L.nsplit > 1 && (!p.part || p.part_bytes < fp8_grad_part_bytes(p.T, p.K, p.N, p.r))) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((L.slabs_a + L.slabs_b) * L.nsplit)), block(512);
+  const int jt = (p.r + 15) / 16;
+  {
+    KernelEvents ev(KID_FP8_GRAD);
+    const hipEvent_t e0 = ev.start(), e1 = ev.stop();
+    if (jt == 1) hipExtLaunchKernelGGL(k_fp8_grad<1>, grid, block, 0, stream, e0, e1, 0, L);
+    else if (jt == 2) hipExtLaunchKernelGGL(k_fp8_grad<2>, grid, block, 0, stream, e0, e1, 0, L);
+    else if (jt <= 4) hipExtLaunchKernelGGL(k_fp8_grad<4>, grid, block, 0, stream, e0, e1, 0, L);
+    else hipExtLaunchKernelGGL(k_fp8_grad<8>, grid, block, 0, stream, e0, e1, 0, L);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || L.nsplit == 1) return e;
+  const int64_t n = (int64_t)p.r * (p.K + p.N);
+  KernelEvents ev(KID_REDUCE);
+  hipExtLaunchKernelGGL(k_fp8_grad_sum, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream, ev.start(),
+                        ev.stop(), 0, L);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -22,6 +22,11 @@ enum KernelId : int {
   KID_ADAMW,
   KID_DROPOUT,
   KID_DECODE_SUM,
+  KID_FP8_QUANTIZE,
+  KID_FP8_DEQUANTIZE,
+  KID_FP8_GEMM,
+  KID_FP8_DOWN,
+  KID_FP8_GRAD,
   KID_COUNT
 };
 

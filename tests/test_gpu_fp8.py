@@ -1,0 +1,313 @@
+"""The 8-bit forms and the linear layer on an 8-bit weight, through the C ABI:
+codes and scales bit for bit against the oracle, outputs and gradients against
+the oracle in 64 bits within bounds that count roundings.
+
+Bounds, per element, mag being the same expression over absolute values:
+  Y, dX (bf16): 2^-8 |want| for the output's rounding, and 2^-10 mag: the
+    matrix units drop what is below 2^-13 of the largest of eight products, at
+    most 7 * 2^-13 of mag; the fp32 additions ((K + r) / 8 of them, 2^-24
+    each) and the hi/lo pair of the rank-r term (2^-16) stay below the
+    remaining 2^-13 for a contraction up to 8192.
+  U: K 2^-24 mag (one fp32 rounding per product at most).
+  dA, dB: (N + T + 16) 2^-24 mag, the fp32 sums of G (over N) and over T; mag
+    is over |dY| |B| (or |U| as given), 16 for the scaling and the three-term
+    split.
+"""
+
+import numpy as np
+import pytest
+
+from gpu_helpers import dev_bf16, say
+from oracle import fp8 as of8
+from oracle.bf16 import bits_to_float, float_to_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _q():
+    import nf4_bit_quantized_amd as q
+    return q
+
+
+def _activations(rng, T, K):
+    x = rng.normal(size=(T, K)) * np.exp(0.5 * rng.normal(size=(T, 1)))
+    x[:, rng.integers(0, K, max(1, K // 200))] *= 20.0
+    return float_to_bits(x.astype(np.float32))
+
+
+def _layer(N, K, T, r, seed):
+    """Inputs of a layer: bf16 bits and the weight in fp32."""
+    rng = np.random.default_rng(seed)
+    return {"W": (rng.normal(size=(N, K)) * 0.02).astype(np.float32), "X": _activations(rng, T, K),
+            "A": float_to_bits((rng.normal(size=(r, K)) / max(r, 1)).astype(np.float32)),
+            "B": float_to_bits((rng.normal(size=(N, r)) * 0.01).astype(np.float32)),
+            "dY": float_to_bits(rng.normal(size=(T, N)).astype(np.float32))}
+
+
+def _within(got, want, mag, c, half=2.0 ** -8):
+    got = got.detach().double().cpu().numpy()
+    bound = half * np.abs(want) + c * mag + 1e-38
+    worst = float(np.max(np.abs(got - want) / bound, initial=0.0))
+    return worst
+
+
+# ---------------------------------------------------------------------------
+# forms
+# ---------------------------------------------------------------------------
+
+FORMS = [(1, 64, 1), (3, 128, 1), (17, 576, 1), (5, 4096, 1), (64, 64, 128), (130, 320, 128), (257, 1088, 128),
+         (1, 192, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols,br", FORMS)
+def test_form_is_the_oracles(rows, cols, br, dtype):
+    import torch
+    q = _q()
+    say(f"form {rows}x{cols} block_rows {br} {dtype}")
+    t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    M = torch.from_numpy(np.random.default_rng(rows + cols).normal(size=(rows, cols)).astype(np.float32)).to(t)
+    M[0, ::7] *= 1000.0
+    want_c, want_s = of8.quantize(M.double().numpy(), br)
+    codes, scales = q.qlora_quantize_fp8(M.cuda(), block_rows=br)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    back = q.qlora_dequantize_fp8(codes, scales, block_rows=br)
+    np.testing.assert_array_equal(back.double().cpu().numpy(), of8.dequantize(want_c, want_s, br))
+
+
+def test_form_of_every_bf16_value():
+    """All finite bf16 values, sorted by size so that each block holds neighbours, and all of one sign bit apart."""
+    import torch
+    q = _q()
+    bits = np.arange(0x7F80, dtype=np.uint16)
+    bits = np.concatenate([bits, bits | 0x8000]).reshape(-1, 128)
+    M = bits_to_float(bits)
+    want_c, want_s = of8.quantize(M)
+    codes, scales = q.qlora_quantize_fp8(dev_bf16(bits))
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    back = q.qlora_dequantize_fp8(codes, scales).double().cpu().numpy()
+    v = of8.dequantize(want_c, want_s)
+    np.testing.assert_array_equal(back, bits_to_float(float_to_bits(v.astype(np.float32))))
+
+
+def test_form_of_extremes():
+    """Zeros, subnormals, the largest finite value and what is not finite, in blocks of their own and mixed."""
+    import torch
+    q = _q()
+    rng = np.random.default_rng(5)
+    M = rng.normal(size=(8, 640)).astype(np.float32)
+    M[0] = 0.0
+    M[1, :128] = 1e-45
+    M[1, 128:256] = np.float32(3.4028235e38)
+    M[2, ::3] = np.nan
+    M[3, 5], M[3, 200], M[3, 639] = np.inf, -np.inf, np.nan
+    M[4, :128] = np.inf
+    M[5, :128] = [448.0, -448.0] * 64
+    M[6, :128] *= np.float32(1e-38)
+    M[7, 0] = np.nextafter(np.float32(448), np.float32(449))
+    want_c, want_s = of8.quantize(M)
+    codes, scales = q.qlora_quantize_fp8(torch.from_numpy(M).cuda())
+    codes, scales = codes.cpu().numpy(), scales.cpu().numpy()
+    np.testing.assert_array_equal(scales, want_s)
+    nan = np.isnan(of8.e4m3_values()[want_c])
+    np.testing.assert_array_equal(np.isnan(of8.e4m3_values()[codes]), nan)
+    np.testing.assert_array_equal(codes[~nan], want_c[~nan])
+
+
+def test_rows_of_a_form_are_the_form_of_the_rows():
+    import torch
+    q = _q()
+    M = torch.randn((50, 704), device="cuda", dtype=torch.bfloat16)
+    codes, scales = q.qlora_quantize_fp8(M)
+    c2, s2 = q.qlora_quantize_fp8(M[13:40].contiguous())
+    assert torch.equal(codes[13:40], c2) and torch.equal(scales[13:40], s2)
+    c3, s3 = q.qlora_quantize_fp8(M[:0])
+    assert c3.shape == (0, 704) and s3.shape == (0, 8)
+    assert q.qlora_dequantize_fp8(c3, s3).shape == (0, 704)
+
+
+# ---------------------------------------------------------------------------
+# layer
+# ---------------------------------------------------------------------------
+
+# (d_out, d_in, T, r)
+LAYERS = [
+    (64, 64, 1, 8),         # the smallest
+    (256, 256, 16, 8),
+    (192, 320, 7, 3),       # half blocks in every direction, odd rank
+    (320, 192, 33, 0),      # base alone
+    (576, 448, 100, 128),   # the largest rank
+    (448, 1088, 129, 20),   # rank a multiple of 4 only
+    (1024, 2048, 1, 64),    # one token
+    (2048, 1024, 16, 16),
+    (1024, 1024, 17, 64),
+    (512, 512, 600, 24),    # several token tiles
+    (1088, 576, 1100, 64),  # many tokens
+]
+
+
+def _forms(inp):
+    import torch
+    q = _q()
+    Wc, Ws = q.qlora_quantize_fp8(torch.from_numpy(inp["W"]).cuda(), block_rows=128)
+    Xc, Xs = q.qlora_quantize_fp8(dev_bf16(inp["X"]))
+    W = of8.dequantize(Wc.cpu().numpy(), Ws.cpu().numpy(), 128)
+    X = of8.dequantize(Xc.cpu().numpy(), Xs.cpu().numpy())
+    return (Wc, Ws, Xc, Xs), W, X
+
+
+@pytest.mark.parametrize("N,K,T,r", LAYERS)
+def test_layer(N, K, T, r):
+    import torch
+    q = _q()
+    say(f"fp8 layer {N}x{K} T {T} r {r}")
+    alpha = 16.0
+    inp = _layer(N, K, T, r, seed=N + K + T + r)
+    forms, W, X = _forms(inp)
+    A, B = (dev_bf16(inp["A"]), dev_bf16(inp["B"])) if r else (None, None)
+    dY = dev_bf16(inp["dY"])
+    Ah, Bh, dYh = (bits_to_float(inp[k]) for k in ("A", "B", "dY"))
+    Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, alpha)
+    wY, wU = of8.forward(W, X, Ah, Bh, alpha, r)
+    mY, mU = of8.forward(np.abs(W), np.abs(X), np.abs(Ah), np.abs(Bh), alpha, r)
+    assert Y.shape == (T, N) and Y.dtype == torch.bfloat16
+    assert _within(Y, wY, mY, 2.0 ** -10) <= 1.0
+    if r:
+        assert _within(U, wU, mU, K * 2.0 ** -24, half=0.0) <= 1.0
+    else:
+        assert U is None
+
+    dX, dA, dB = q.qlora_fp8_linear_bwd(*forms, A, B, alpha, dY, U_in=U)
+    wX, wA, wB = of8.backward(W, X, Ah, Bh, dYh, alpha, r)
+    # absolute values: the form of |dY| is |form of dY|
+    mX, mA, mB = of8.backward(np.abs(W), np.abs(X), np.abs(Ah), np.abs(Bh), np.abs(dYh), alpha, r)
+    assert _within(dX, wX, mX, 2.0 ** -10) <= 1.0
+    if r:
+        c = (N + T + 16) * 2.0 ** -24
+        assert _within(dA, wA, mA, c, half=0.0) <= 1.0
+        assert _within(dB, wB, mB, c + K * 2.0 ** -24, half=0.0) <= 1.0
+        # U recomputed from the form: dB within the same bound, dA and dX the same bits
+        dX2, dA2, dB2 = q.qlora_fp8_linear_bwd(*forms, A, B, alpha, dY)
+        assert torch.equal(dX2, dX) and torch.equal(dA2, dA)
+        assert _within(dB2, wB, mB, c + K * 2.0 ** -24, half=0.0) <= 1.0
+        # accumulation: one fp32 addition
+        a0, b0 = torch.randn_like(dA), torch.randn_like(dB)
+        _, dA3, dB3 = q.qlora_fp8_linear_bwd(*forms, A, B, alpha, dY, U_in=U, dA=a0.clone(), dB=b0.clone(),
+                                             want_dx=False, accumulate=True)
+        assert torch.equal(dA3, a0 + dA) and torch.equal(dB3, b0 + dB)
+    else:
+        assert dA is None and dB is None
+    # again: the same bits
+    Y2, _ = q.qlora_fp8_linear_fwd(*forms, A, B, alpha)
+    assert torch.equal(Y, Y2)
+
+
+def test_no_tokens():
+    import torch
+    q = _q()
+    inp = _layer(128, 192, 0, 8, seed=1)
+    forms, _, _ = _forms(inp)
+    A, B, dY = dev_bf16(inp["A"]), dev_bf16(inp["B"]), dev_bf16(inp["dY"])
+    Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0)
+    assert Y.shape == (0, 128) and U.shape == (0, 8)
+    dX, dA, dB = q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY)
+    assert dX.shape == (0, 192) and not dA.any() and not dB.any()
+    a0, b0 = torch.randn_like(dA), torch.randn_like(dB)
+    _, dA, dB = q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY, dA=a0.clone(), dB=b0.clone(), accumulate=True)
+    assert torch.equal(dA, a0) and torch.equal(dB, b0)
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_what_is_not_finite_stays_in_its_token(T):
+    """A NaN or an infinity in one token's input makes that token's outputs NaN and changes no other bit."""
+    import torch
+    q = _q()
+    inp = _layer(192, 320, T, 8, seed=T)
+    forms, _, _ = _forms(inp)
+    A, B = dev_bf16(inp["A"]), dev_bf16(inp["B"])
+    Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0)
+    X = dev_bf16(inp["X"])
+    X[3, 300] = float("inf")
+    Xc, Xs = q.qlora_quantize_fp8(X)
+    Y2, U2 = q.qlora_fp8_linear_fwd(forms[0], forms[1], Xc, Xs, A, B, 16.0)
+    keep = torch.arange(T, device="cuda") != 3
+    assert torch.equal(Y2[keep], Y[keep]) and torch.equal(U2[keep], U[keep])
+    assert Y2[3].isnan().all() and U2[3].isnan().all()
+
+
+def test_rows_behind_the_last_token_stay():
+    """Outputs given as the first rows of larger buffers: what lies behind is left as it was."""
+    import torch
+    q = _q()
+    inp = _layer(320, 448, 37, 12, seed=9)
+    forms, _, _ = _forms(inp)
+    A, B, dY = dev_bf16(inp["A"]), dev_bf16(inp["B"]), dev_bf16(inp["dY"])
+    Yb = torch.full((64, 320), 7.0, dtype=torch.bfloat16, device="cuda")
+    Ub = torch.full((64, 12), 7.0, device="cuda")
+    Xb = torch.full((64, 448), 7.0, dtype=torch.bfloat16, device="cuda")
+    q.qlora_fp8_linear_fwd(*forms, A, B, 16.0, Y=Yb[:37], U_out=Ub[:37])
+    q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY, U_in=Ub[:37], dX=Xb[:37])
+    for b in (Yb, Ub, Xb):
+        assert (b[37:] == 7.0).all() and not (b[:37] == 7.0).all()
+
+
+@pytest.mark.parametrize("N,K,T,r", [(256, 320, 3, 8), (512, 448, 200, 16), (1024, 1024, 1100, 64)])
+def test_given_workspace_of_just_the_size(N, K, T, r):
+    """The workspace of the queried size is enough, its contents do not matter and nothing behind it is written."""
+    import torch
+    q = _q()
+    inp = _layer(N, K, T, r, seed=11)
+    forms, _, _ = _forms(inp)
+    A, B, dY = dev_bf16(inp["A"]), dev_bf16(inp["B"]), dev_bf16(inp["dY"])
+    Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0)
+    ref = q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY)
+    for n, call, want in (
+            (q.qlora_fp8_fwd_workspace_bytes(N, K, T, r), lambda w: q.qlora_fp8_linear_fwd(*forms, A, B, 16.0, workspace=w), (Y, U)),
+            (q.qlora_fp8_bwd_workspace_bytes(N, K, T, r), lambda w: q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY, workspace=w), ref)):
+        for fill in (0, 255):
+            buf = torch.full((n + 4096,), fill, dtype=torch.uint8, device="cuda")
+            got = call(buf[:n])
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            assert (buf[n:] == fill).all()
+
+
+def test_other_stream_and_graph_replays():
+    """The calls on a stream of their own, then captured and replayed with other inputs and eager work between."""
+    import torch
+    q = _q()
+    T, N, K, r = 200, 512, 448, 16
+    ins = [_layer(N, K, T, r, seed=20 + k) for k in range(3)]
+    forms, _, _ = _forms(ins[0])
+    A, B = dev_bf16(ins[0]["A"]), dev_bf16(ins[0]["B"])
+    X, dY = torch.empty((T, K), dtype=torch.bfloat16, device="cuda"), torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+
+    def step(X, dY, stream=None):
+        Xc, Xs = q.qlora_quantize_fp8(X, stream=stream)
+        Y, U = q.qlora_fp8_linear_fwd(forms[0], forms[1], Xc, Xs, A, B, 16.0, stream=stream)
+        return (q.qlora_dequantize_fp8(Xc, Xs, stream=stream), Y, U) + q.qlora_fp8_linear_bwd(
+            forms[0], forms[1], Xc, Xs, A, B, 16.0, dY, U_in=U, stream=stream)
+
+    side = torch.cuda.Stream()
+    X.copy_(dev_bf16(ins[0]["X"]))
+    dY.copy_(dev_bf16(ins[0]["dY"]))
+    torch.cuda.synchronize()
+    on_side = step(X, dY, side)
+    side.synchronize()
+    eager = step(X, dY)
+    assert all(torch.equal(a, b) for a, b in zip(on_side, eager))
+    with torch.cuda.stream(side):
+        step(X, dY)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(X, dY)
+    for rep in range(4):
+        inp = ins[rep % 3]
+        X.copy_(dev_bf16(inp["X"]))
+        dY.copy_(dev_bf16(inp["dY"]))
+        graph.replay()
+        want = step(dev_bf16(inp["X"]), dev_bf16(inp["dY"]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), rep

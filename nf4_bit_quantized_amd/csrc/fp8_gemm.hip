@@ -19,6 +19,7 @@
 // the 2^-4 that each code is already rounded by and the 2^-8 of the result.
 #include "dma.hpp"
 #include "fp8.hpp"
+#include "fp8_tail.hpp"
 #include "trace.hpp"
 
 namespace qlora {
@@ -50,25 +51,6 @@ struct Fp8Launch {
   int32_t steps, steps_per_split;
   int64_t out_cols;    // features: Nw, or Kw for dx
 };
-
-// Eight consecutive tail columns c .. c+7 of feature row n.
-__device__ __forceinline__ bf16x8_t tail_weight(const Fp8Params& p, int64_t n, int64_t rows, int c) {
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (n < rows) {
-    if (p.bt_pair) {
-      v = *reinterpret_cast<const u32x4_t*>(p.Bt + n * p.ldh + c);
-    } else if (c < 2 * p.r) {
-      v = *reinterpret_cast<const u32x4_t*>(p.Bt + n * p.r + (c < p.r ? c : c - p.r));
-    }
-  }
-  return __builtin_bit_cast(bf16x8_t, v);
-}
-
-__device__ __forceinline__ bf16x8_t tail_token(const Fp8Params& p, int64_t t, int c) {
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (t < p.T) v = *reinterpret_cast<const u32x4_t*>(p.At + t * p.ldh + c);
-  return __builtin_bit_cast(bf16x8_t, v);
-}
 
 // ---------------------------------------------------------------------------
 // 128 features x 128 tokens, four waves of 64 x 64, contraction steps of 128
@@ -277,6 +259,7 @@ size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx) {
 }
 
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
+  if (((p.T + 255) / 256) * (((p.dx ? p.Kw : p.Nw) + 255) / 256) >= 128) return launch_fp8_wide(p, stream);
   Fp8Launch L{};
   L.p = p;
   const int64_t feats = p.dx ? p.Kw : p.Nw, len = p.dx ? p.Nw : p.Kw;

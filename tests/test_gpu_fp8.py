@@ -145,6 +145,11 @@ LAYERS = [
     (1024, 1024, 17, 64),
     (512, 512, 600, 24),    # several token tiles
     (1088, 576, 1100, 64),  # many tokens
+    (4096, 320, 2100, 8),   # 256 x 256 tiles forward, ragged tokens, half a block of contraction
+    (4160, 1024, 2049, 12),  # one token and 64 features past whole tiles
+    (448, 4096, 2100, 24),  # 256 x 256 tiles backward
+    (1024, 4160, 2304, 64),
+    (64, 4096, 2304, 8),    # a contraction of 64
 ]
 
 

@@ -13,7 +13,6 @@ the environment variable ``QLORA_NF4_LIBRARY`` names (for example a build of
 the same sources with host-side sanitizers).
 """
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -680,36 +679,57 @@ def qlora_merge_lora(packed, codes, consts, A, B, alpha: float, W_merged=None, s
 FP8_BLOCK = 128
 
 
-@contextlib.contextmanager
-def _launch_on(device, stream, name: str):
-    """Make ``device`` and ``stream`` (None: the device's current one) current; yields the stream's handle."""
-    import torch
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
-    with torch.cuda.device(device):
+class _LaunchOn:
+    """Makes ``device`` and ``stream`` (None: the device's current one) current; ``handle`` is the stream's."""
+
+    __slots__ = ("handle", "_device", "_stream")
+
+    def __init__(self, device, stream, name: str):
+        import torch
+        self._device = self._stream = None
+        if device.index != torch.cuda.current_device():
+            self._device = torch.cuda.device(device)
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+            # torch.cuda.current_stream(device).cuda_stream, without the Stream object (2 us of a call's 10)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            return
+        if stream.device != device:
+            raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
+        self._stream = torch.cuda.stream(stream)
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
 
 
 def _one_device(name: str, *tensors):
     """The GPU that every given tensor is on (None entries are left out)."""
-    _need_cuda(*tensors, name=name)
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"{name}: the tensors are on {len(devices)} devices: {sorted(map(str, devices))}")
-    return devices.pop()
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.device
+        if d.type != "cuda":
+            raise ValueError(f"{name}: tensors must be on the GPU")
+        if device is None:
+            device = d
+        elif d != device:
+            raise ValueError(f"{name}: the tensors are on different devices: {device} and {d}")
+    return device
 
 
-def _fp8_shapes(rows: int, cols: int, block_rows: int):
-    """Shapes of codes and scales."""
-    a, b = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().qlora_fp8_sizes(int(rows), int(cols), int(block_rows), ctypes.byref(a), ctypes.byref(b)),
-           "qlora_fp8_sizes")
-    ld = -(-cols // 512) * 4
-    return (rows, cols), (b.value // ld, ld)
+def _scales_shape(rows: int, cols: int, block_rows: int):
+    return -(-rows // block_rows), -(-cols // 512) * 4
 
 
 def qlora_fp8_sizes(rows: int, cols: int, block_rows: int = 1) -> Tuple[int, int]:
@@ -727,7 +747,9 @@ def _check_form(codes, scales, block_rows: int, name: str):
         raise ValueError(f"{name}: codes and scales are required")
     if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
         raise ValueError(f"{name}: codes must be a contiguous 2-D uint8 tensor")
-    _check_in(scales, _fp8_shapes(codes.shape[0], codes.shape[1], block_rows)[1], torch.uint8, f"{name}: scales")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"{name}: block_rows must be 1 or {FP8_BLOCK}")
+    _check_in(scales, _scales_shape(codes.shape[0], codes.shape[1], block_rows), torch.uint8, f"{name}: scales")
 
 
 def qlora_quantize_fp8(M, block_rows: int = 1, codes=None, scales=None, stream=None):
@@ -737,23 +759,28 @@ def qlora_quantize_fp8(M, block_rows: int = 1, codes=None, scales=None, stream=N
     128: a scale per 128 x 128 block (a weight).  ``codes.view(torch.float8_e4m3fn)`` are the codes' values,
     ``scales.view(torch.float8_e8m0fnu)`` the scales'."""
     import torch
-    fmts = {torch.float32: QLORA_W_F32, torch.bfloat16: QLORA_W_BF16, torch.float16: QLORA_W_F16}
     _matrix(M, "M")
-    if M.dtype not in fmts:
+    dt = M.dtype
+    fmt = (QLORA_W_BF16 if dt == torch.bfloat16 else QLORA_W_F32 if dt == torch.float32
+           else QLORA_W_F16 if dt == torch.float16 else None)
+    if fmt is None:
         raise ValueError("M must be a float32, bfloat16 or float16 tensor")
     if not M.is_contiguous():
         raise ValueError("M must be contiguous")
-    shape_c, shape_s = _fp8_shapes(M.shape[0], M.shape[1], block_rows)
-    _check_out(codes, shape_c, torch.uint8, "codes")
+    rows, cols = M.shape
+    if cols % 64 != 0 or block_rows not in (1, FP8_BLOCK):
+        qlora_fp8_sizes(rows, cols, block_rows)     # refuses it
+    shape_s = _scales_shape(rows, cols, block_rows)
+    _check_out(codes, (rows, cols), torch.uint8, "codes")
     _check_out(scales, shape_s, torch.uint8, "scales")
     device = _one_device("qlora_quantize_fp8", M, codes, scales)
-    with _launch_on(device, stream, "qlora_quantize_fp8") as st:
+    with _LaunchOn(device, stream, "qlora_quantize_fp8") as st:
         if codes is None:
-            codes = torch.empty(shape_c, dtype=torch.uint8, device=device)
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=device)
         if scales is None:
             scales = torch.empty(shape_s, dtype=torch.uint8, device=device)
-        _check(lib().qlora_quantize_fp8(M.shape[0], M.shape[1], int(block_rows), _ptr(M), fmts[M.dtype], _ptr(codes),
-                                        _ptr(scales), st), "qlora_quantize_fp8")
+        _check(lib().qlora_quantize_fp8(rows, cols, block_rows, M.data_ptr(), fmt, codes.data_ptr(),
+                                        scales.data_ptr(), st), "qlora_quantize_fp8")
     return codes, scales
 
 
@@ -763,7 +790,7 @@ def qlora_dequantize_fp8(codes, scales, block_rows: int = 1, M_hat=None, stream=
     _check_form(codes, scales, block_rows, "qlora_dequantize_fp8")
     _check_out(M_hat, codes.shape, torch.bfloat16, "M_hat")
     device = _one_device("qlora_dequantize_fp8", codes, scales, M_hat)
-    with _launch_on(device, stream, "qlora_dequantize_fp8") as st:
+    with _LaunchOn(device, stream, "qlora_dequantize_fp8") as st:
         if M_hat is None:
             M_hat = torch.empty(tuple(codes.shape), dtype=torch.bfloat16, device=device)
         _check(lib().qlora_dequantize_fp8(codes.shape[0], codes.shape[1], int(block_rows), _ptr(codes), _ptr(scales),
@@ -803,7 +830,7 @@ def qlora_fp8_linear_fwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: floa
     _check_out(U_out, (T, r), torch.float32, "U_out")
     device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, Y, U_out, workspace)
     nbytes = qlora_fp8_fwd_workspace_bytes(d_out, d_in, T, r)
-    with _launch_on(device, stream, name) as st:
+    with _LaunchOn(device, stream, name) as st:
         if Y is None:
             Y = torch.empty((T, d_out), dtype=torch.bfloat16, device=device)
         if U_out is None and want_u and r > 0:
@@ -846,7 +873,7 @@ def qlora_fp8_linear_bwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: floa
     _grad_buffers(dX, dA, dB, T, d_out, d_in, r, accumulate)
     device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, dY, U_in, dX, dA, dB, workspace)
     nbytes = qlora_fp8_bwd_workspace_bytes(d_out, d_in, T, r)
-    with _launch_on(device, stream, name) as st:
+    with _LaunchOn(device, stream, name) as st:
         if dX is None and want_dx:
             dX = torch.empty((T, d_in), dtype=torch.bfloat16, device=device)
         if r > 0 and dA is None:
@@ -883,7 +910,7 @@ def qlora_linear_bwd_checkpoint(packed, codes, consts, X_codes, X_scales, A, B, 
     n = ctypes.c_size_t()
     _check(lib().qlora_checkpoint_workspace_bytes(ctypes.byref(d), T, r, ctypes.byref(n)),
            "qlora_checkpoint_workspace_bytes")
-    with _launch_on(device, stream, name) as st:
+    with _LaunchOn(device, stream, name) as st:
         if dX is None and want_dx:
             dX = torch.empty((T, d_in), dtype=torch.bfloat16, device=device)
         if r > 0 and dA is None:

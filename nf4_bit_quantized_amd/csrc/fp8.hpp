@@ -41,8 +41,6 @@ struct Fp8Params {
 };
 size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx);
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream);
-// the product on 256 x 256 tiles (fp8_wide.hip; dx == 0), which launch_fp8_product picks
-hipError_t launch_fp8_wide(const Fp8Params& p, hipStream_t stream);
 
 // The pair operand of a tail: out [rows][ldh] = (V | V | 0), V [rows][r] being
 // B itself (transposed == 0: B [rows][r]) or A's transpose (1: A [r][rows]).

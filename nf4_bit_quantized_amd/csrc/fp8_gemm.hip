@@ -4,23 +4,53 @@
 //   C[t][n] = bf16( sum_k X[t][k] W[n][k] + sum_c At[t][c] Bt[n][c] )
 //   C[t][k] = bf16( sum_n X[t][n] W[n][k] + sum_c At[t][c] Bt[k][c] )   (dx)
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by 128 x 16 codes and
-// both operands' scales: one instruction is one block of 128, and since a
-// block's scale is the same for all its 128 elements, the order in which they
-// are spread over the lanes is free as long as both operands use the same one.
-// Lane l holds 32 codes of row (column) l % 16 and its scale byte; here lane
-// group g = l / 16 takes the 16-byte chunks g and g + 4 of the 128.  The first
-// operand is the weight, so a lane's four results are four consecutive output
-// features of one token.
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 by 64 x 32 codes and both
+// operands' scales, half a block of 128: lane l holds row (column) l % 32 and
+// 32 consecutive codes, those from 32 (l / 32) of the 64, and its row's scale
+// byte.  The first operand is the weight, so four consecutive results of a
+// lane are four consecutive output features of one token.
 //
 // Precision: the unit adds products in groups of eight aligned to the group's
 // largest, dropping what lies below 2^-13 of it (measured), and everything
 // after that in fp32.  A dropped bit is at most 2^-13 of one product, against
 // the 2^-4 that each code is already rounded by and the 2^-8 of the result.
+//
+// Tiles of 256 x 256: one workgroup of four waves per CU, one wave per SIMD
+// with 512 registers.  Wave (a, b) owns features 128 a .. +127 and tokens 128 b
+// .. +127: 4 x 4 tiles of 32 x 32, 256 fp32 accumulators a lane.  Tiles of 128
+// x 128, two workgroups per CU, are half of that each way (plan_product).
+//
+// What bounds such a tile is how fast operands reach the matrix units, which a
+// step of 64 occupies for 1024 cycles at the full rate.  At 4096 x 8192 x 8192
+// (one box; TFLOP/s with the outputs of every variant in place):
+//   2700  this kernel: both operands copied in rows of 128 bytes
+//   2430  copies in rows of 64 bytes: as many bytes, twice the L2 requests
+//   2290  the weight's fragments loaded from global memory into registers (a
+//         fragment's neighbouring lanes lie in different rows, 64 lookups a load)
+//   3060  without the copies and the fragment reads (matrix units, their
+//         scales, barriers and the output alone)
+// Starting tiles at different places of the contraction costs 2-25%: the 32
+// tiles of an XCD live off each other's rows in its L2.
+//
+// Pipeline, per wave and step u: both operands are copied into a ring of five
+// LDS slots, each 128 of the contraction (two steps) of one operand, X two
+// pairs of steps ahead and W one and a half; a step's fragments are read
+// during the step before it.  The one barrier of a pair stands in its second
+// step, behind the second MFMA: by then every wave has waited for its copies
+// of the next pair and for its last fragments of this one, whose slots the
+// next copies refill.
+//
+// Rows of a slot are 128 bytes, chunk c of row R at c ^ R % 8 ^ R / 8 % 2: the
+// 16 lanes of a fragment read (16 rows, one chunk) fall on distinct bank
+// groups.  The weight of dx, whose contraction runs down its rows, is kept as
+// [128 rows][256 columns] with piece c of row R at c ^ 2 (R % 8), and read with
+// transposing reads (16 lanes: 8 rows of 16 bytes, a lane receives a column).
 #include "dma.hpp"
 #include "fp8.hpp"
 #include "fp8_tail.hpp"
 #include "trace.hpp"
+
+#include <type_traits>
 
 namespace qlora {
 namespace {
@@ -28,269 +58,558 @@ namespace {
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef int v2i_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) v2i_t lds_v2i_t;
 typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
-using dma::copy16;
-using dma::kOob;
-using dma::rsrc;
-using dma::v4i_t;
-using dma::wait_vm;
+typedef const __attribute__((address_space(4))) uint32_t* const_u32;
 
-__device__ __forceinline__ f32x4_t mfma8(v8i_t a, v8i_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
-}
+constexpr uint32_t kSlots = 5;
 
-__device__ __forceinline__ v8i_t join(u32x4_t a, u32x4_t b) {
-  return v8i_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
-struct Fp8Launch {
+struct WideLaunch {
   Fp8Params p;
-  int32_t mt, nt;      // feature tiles, token tiles
-  int32_t nsplit;      // contraction ranges
-  int32_t steps, steps_per_split;
-  int64_t out_cols;    // features: Nw, or Kw for dx
+  int32_t mt, nt, group;  // token tiles, feature tiles, token tiles walked together
+  int32_t f_begin;        // the first feature
+  int32_t nsplit;         // contraction ranges of a tile
+  uint32_t split_steps;   // steps of a range, a multiple of 8
 };
 
-// ---------------------------------------------------------------------------
-// 128 features x 128 tokens, four waves of 64 x 64, contraction steps of 128
-// double-buffered in LDS.
-// ---------------------------------------------------------------------------
-constexpr int BT = 128;
-constexpr int kTileBytes = BT * 128;
-constexpr int kOutLd = BT + 8;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf(const void* p, int64_t bytes) {
+  const int32_t n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (int32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, 0x00020000);
+}
 
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+template <int Q>
+__device__ __forceinline__ f32x16_t mfma8(v8i_t a, v8i_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, Q, (int)sa, Q, (int)sb);
+}
 
-template <bool DX>
-__global__ __launch_bounds__(256) void k_fp8_tile(Fp8Launch L) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kTileBytes];
+// A copy into LDS that the compiler does not count (see dma.hpp): behind one
+// that it knows of, it would wait for every copy in flight before a
+// transposing read.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16_uncounted(dma::v4i_t r, uint32_t voff, uint32_t soff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(voff), "s"(r), "s"(soff)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// DX: the weight's contraction runs down its rows; S: 32 x 32 tiles of a wave
+// each way (4: tiles of 256 x 256, a workgroup per CU; 2: 128 x 128, two).
+template <bool DX, int S>
+__device__ __forceinline__ void product(const WideLaunch& L) {
+  constexpr int WT = 64 * S, WF = 64 * S;       // tokens and features of the tile
+  constexpr uint32_t kSlot = WT * 128;
+  constexpr int kLds = kSlots * kSlot;
+  constexpr int kOutLd = WF + 8;
+  constexpr int M = S * S;                      // MFMAs of a step
+  constexpr int NR = 4 * S;                     // its fragment reads
+  constexpr int NC = 2 * S;                     // copies of an operand's pair of steps, a wave
+  constexpr int BAR = S == 4 ? 1 : 0;           // the barrier's place among the MFMAs
+  static_assert(WT * kOutLd * 2 <= kLds, "the output tile fits over the slots");
+  struct Frags {
+    u32x4_t x[S][2], w[S][2];
+  };
+  // the n-th slot after the one at byte o
+  auto slot_after = [](uint32_t o, uint32_t n) { return o + n * kSlot < kLds ? o + n * kSlot : o + n * kSlot - kLds; };
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const Fp8Params& p = L.p;
+  // runs of consecutive tiles go to one XCD; in their order, groups of token
+  // tiles are walked feature tile by feature tile
+  const uint32_t mt = (uint32_t)L.mt, nt = (uint32_t)L.nt, gm = (uint32_t)L.group;
+  const uint32_t run = (mt * nt * (uint32_t)L.nsplit + 7) / 8;
+  uint32_t order = blockIdx.x % 8 * run + blockIdx.x / 8;
+  if (order >= mt * nt * (uint32_t)L.nsplit) return;
+  // the ranges of the contraction follow each other, each over all the tiles
+  const uint32_t split = __builtin_amdgcn_readfirstlane(order / (mt * nt));
+  order -= split * (mt * nt);
+  const uint32_t first = order / (gm * nt) * gm;
+  const uint32_t rows = mt - first < gm ? mt - first : gm;
+  const uint32_t in_group = order - first * nt;
+  // (in scalar registers: they go into the buffer resources)
+  const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane((first + in_group % rows) * WT);
+  const int64_t f0 = (int64_t)__builtin_amdgcn_readfirstlane(L.f_begin + in_group / rows * WF);
+
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int i = lane & 15, g = lane >> 4;
-  const int wf = (wave & 1) * 64, wt = (wave >> 1) * 64;  // the wave's features and tokens
-  int b = (int)blockIdx.x;
-  const int split = b / (L.mt * L.nt);
-  b -= split * (L.mt * L.nt);
-  const int64_t f0 = (int64_t)(b % L.mt) * BT, t0 = (int64_t)(b / L.mt) * BT;
-  const int64_t len = DX ? p.Nw : p.Kw;       // contraction
-  const int64_t feats = DX ? p.Kw : p.Nw;
-  const int s_begin = split * L.steps_per_split;
-  const int s_end = s_begin + L.steps_per_split < L.steps ? s_begin + L.steps_per_split : L.steps;
+  const int wf = 32 * S * (wave & 1), wt = 32 * S * (wave >> 1);
+  const int g = lane >> 5, c32 = lane & 31, i16 = lane & 15;
+  const int64_t len = DX ? p.Nw : p.Kw, feats = DX ? p.Kw : p.Nw;
+  const uint32_t first_step = split * L.split_steps;
+  const uint32_t steps_left = (uint32_t)(len / 64) - first_step;
+  const uint32_t nsteps = __builtin_amdgcn_readfirstlane(steps_left < L.split_steps ? steps_left : L.split_steps);
+  const int64_t k0 = (int64_t)first_step * 64;  // a multiple of 512: whole dwords of scales
 
-  const v4i_t rx = rsrc(p.X + t0 * len, (p.T - t0) * len);
-  const v4i_t rw = DX ? rsrc(p.W + f0, p.Nw * p.Kw - f0) : rsrc(p.W + f0 * p.Kw, (p.Nw - f0) * p.Kw);
-  const uint32_t lds0 = LDS_ADDR(lds);
+  // both operands from the range's first position on
+  const int64_t xbase = t0 * len + k0, wbase = DX ? k0 * p.Kw + f0 : f0 * len + k0;
+  const int64_t xbytes = (p.T - t0) * len - k0, wbytes = p.Nw * p.Kw - wbase;
+  const __amdgpu_buffer_rsrc_t rx = buf(p.X + xbase, xbytes), rw = buf(p.W + wbase, wbytes);
+  const dma::v4i_t ax = dma::rsrc(p.X + xbase, xbytes), aw = dma::rsrc(p.W + wbase, wbytes);  // dx
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(LDS_ADDR(lds));
+  const __amdgpu_buffer_rsrc_t rs = buf(p.Xs, p.T * fp8_scale_ld(len));
 
-  auto issue = [&](int s) {
-    const uint32_t st = lds0 + (uint32_t)((s & 1) * 2 * kTileBytes);
-    const int64_t k0 = (int64_t)s * 128;
+  // copies of a pair of steps: eight kilobytes of each operand a wave.  Rows
+  // past the last token or feature read zeros.
+  uint32_t xoff[NC], woff[NC];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int blk = 4 * wave + q;
-      const int R = 8 * blk + (lane >> 3);
-      const int px = (lane & 7) ^ swz(R);
-      const uint32_t vx = k0 + px * 16 < len && t0 + R < p.T ? (uint32_t)(R * len + k0 + px * 16) : kOob;
-      copy16(rx, vx, st + kTileBytes + blk * 1024);
-      uint32_t vw;
-      if (DX) {
-        const int pw = (lane & 7) ^ (R & 7);
-        vw = k0 + R < p.Nw && f0 + pw * 16 < p.Kw ? (uint32_t)((k0 + R) * p.Kw + pw * 16) : kOob;
-      } else {
-        vw = k0 + px * 16 < len && f0 + R < p.Nw ? (uint32_t)(R * p.Kw + k0 + px * 16) : kOob;
-      }
-      copy16(rw, vw, st + blk * 1024);
-    }
-  };
-
-  f32x4_t acc[4][4];  // [feature tile][token tile]
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[a][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  const int64_t ldx = fp8_scale_ld(len), ldw = fp8_scale_ld(p.Kw);
-  if (s_begin < s_end) issue(s_begin);
-  for (int s = s_begin; s < s_end; ++s) {
-    wait_vm<0>();
-    __syncthreads();
-    uint32_t sx[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t t = t0 + wt + 16 * c + i;
-      sx[c] = p.Xs[(t < p.T ? t : p.T - 1) * ldx + s];
-    }
-    const uint32_t sw = DX ? p.Ws[(int64_t)s * ldw + (f0 >> 7)] : p.Ws[(f0 >> 7) * ldw + s];
-    if (s + 1 < s_end) issue(s + 1);
-    const uint8_t* w = lds + (s & 1) * 2 * kTileBytes;
-    const uint8_t* x = w + kTileBytes;
-    v8i_t fx[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int R = wt + 16 * c + i;
-      fx[c] = join(*reinterpret_cast<const u32x4_t*>(x + R * 128 + ((g ^ swz(R)) << 4)),
-                   *reinterpret_cast<const u32x4_t*>(x + R * 128 + (((g + 4) ^ swz(R)) << 4)));
-    }
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      v8i_t fw;
-      if (DX) {
-        // transposed: column wf + 16a + l%16, rows of chunks g and g + 4; 16
-        // lanes read 8 rows of 16 bytes, lane i receives its column's 8 rows
-        const int piece = (wf >> 4) + a;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int R = (q >> 1) * 64 + 16 * g + 8 * (q & 1) + (i >> 1);
-          const v2i_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (lds_v2i_t*)((lds_u8_t*)w + R * 128 + ((piece ^ (R & 7)) << 4) + 8 * (i & 1)));
-          fw[2 * q] = v[0];
-          fw[2 * q + 1] = v[1];
-        }
-      } else {
-        const int R = wf + 16 * a + i;
-        fw = join(*reinterpret_cast<const u32x4_t*>(w + R * 128 + ((g ^ swz(R)) << 4)),
-                  *reinterpret_cast<const u32x4_t*>(w + R * 128 + (((g + 4) ^ swz(R)) << 4)));
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[a][c] = mfma8(fw, fx[c], acc[a][c], sw, sx[c]);
+  for (int j = 0; j < NC; ++j) {
+    const int R = 16 * S * wave + 8 * j + (lane >> 3);
+    const int chunk = (lane & 7) ^ (lane >> 3) ^ (j & 1);
+    xoff[j] = t0 + R < p.T ? (uint32_t)(R * len + chunk * 16) : dma::kOob;
+    if (DX) {
+      const int n = S == 4 ? 32 * wave + 4 * j + (lane >> 4) : 32 * wave + 8 * j + (lane >> 3);
+      const int piece = S == 4 ? i16 ^ (2 * (n & 7)) : (lane & 7) ^ (n & 6);
+      woff[j] = f0 + piece * 16 < feats ? (uint32_t)(n * p.Kw + piece * 16) : dma::kOob;
+    } else {
+      woff[j] = f0 + R < feats ? (uint32_t)(R * len + chunk * 16) : dma::kOob;
     }
   }
+  const uint32_t wpair = DX ? (uint32_t)(128 * p.Kw) : 128u;
+  const uint32_t pairs = (nsteps + 1) / 2;
+  // copy j (0 .. NC - 1) of X's or W's pair `pr` into a slot
+  auto copy_x = [&](uint32_t pr, uint32_t slot, int j) {
+    const uint32_t at = pr < pairs ? pr : pairs - 1;
+    if (DX) copy16_uncounted(ax, xoff[j], at * 128u, lds0 + slot + kSlot / 4 * wave + 1024 * j);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, xoff[j], at * 128u, 0, 0);
+  };
+  auto copy_w = [&](uint32_t pr, uint32_t slot, int j) {
+    const uint32_t at = pr < pairs ? pr : pairs - 1;
+    if (DX) copy16_uncounted(aw, woff[j], at * wpair, lds0 + slot + kSlot / 4 * wave + 1024 * j);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, woff[j], at * wpair, 0, 0);
+  };
 
-  if (p.r > 0 && split == 0) {
-    for (int c0 = 0; c0 < 2 * p.r; c0 += 32) {
-      bf16x8_t bt[4];
+  // scales: a dword holds the bytes of four blocks, eight steps
+  const uint32_t groups = (nsteps + 7) / 8;
+  uint32_t soff[S];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) bt[c] = tail_token(p, t0 + wt + 16 * c + i, c0 + 8 * g);
+  for (int t = 0; t < S; ++t) {
+    const int64_t row = t0 + wt + 32 * t + c32;
+    soff[t] = (uint32_t)((row < p.T ? row : p.T - 1) * fp8_scale_ld(len) + k0 / 128);
+  }
+  // X's: a dword a group; for dx, whose copies are uncounted and drained by
+  // the wait for a counted load, four dwords in every fourth group (3% faster
+  // there, and as much slower where the copies are counted)
+  auto load_sx = [&](uint32_t gr, int t) {
+    return __builtin_amdgcn_raw_buffer_load_b32(rs, soff[t], (gr < groups ? gr : groups - 1) * 4u, 0);
+  };
+  auto load_sx4 = [&](uint32_t quad, int t) { return __builtin_amdgcn_raw_buffer_load_b128(rs, soff[t], quad * 16u, 0); };
+  // the wave's features lie in one block of the weight: its bytes lie in one
+  // row of the weight's scales, or, for dx, in one column of them
+  const int64_t fb = __builtin_amdgcn_readfirstlane((uint32_t)((f0 + wf < feats ? f0 + wf : f0) / 128));
+  const int64_t ldw = fp8_scale_ld(p.Kw);
+  const uint8_t* ws = p.Ws + (DX ? k0 / 128 * ldw : k0 / 128);
+  struct SwRaw {
+    uint32_t v[4];
+  };
+  auto load_sw = [&](uint32_t gr) {
+    const uint32_t at = gr < groups ? gr : groups - 1;
+    SwRaw r{};
+    if (!DX) {
+      r.v[0] = *(const_u32)(ws + fb * ldw + 4 * at);
+    } else {
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const bf16x8_t wa = tail_weight(p, f0 + wf + 16 * a + i, feats, c0 + 8 * g);
+      for (uint32_t q = 0; q < 4; ++q)
+        r.v[q] = *(const_u32)(ws + (4 * at + q < pairs ? 4 * at + q : pairs - 1) * ldw + (fb & ~3LL));
+    }
+    return r;
+  };
+  auto sw_of = [&](const SwRaw& r) -> uint32_t {
+    if (!DX) return r.v[0];
+    const uint32_t sh = 8 * (uint32_t)(fb & 3);
+    return (r.v[0] >> sh & 0xFFu) | (r.v[1] >> sh & 0xFFu) << 8 | (r.v[2] >> sh & 0xFFu) << 16 | (r.v[3] >> sh) << 24;
+  };
+
+  // fragment reads of half h of a pair; tile t's are 4096 bytes on (dx: rows
+  // 64 h + 8 q are WF (64 h + 8 q) bytes on)
+  const int sw = (c32 & 7) ^ ((c32 >> 3) & 1);
+  uint32_t xpos[2][2], wpos[S];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa, bt[c], acc[a][c], 0, 0, 0);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) xpos[h][e] = (uint32_t)(c32 * 128 + (((4 * h + 2 * g + e) ^ sw) << 4));
+#pragma unroll
+  for (int f = 0; f < S; ++f) {
+    const int piece = (wf >> 4) + 2 * f + ((lane >> 4) & 1);
+    const int swz = S == 4 ? i16 & 14 : (i16 >> 1) & 6;
+    wpos[f] = (uint32_t)((32 * g + (i16 >> 1)) * WF + ((piece ^ swz) << 4) + 8 * (i16 & 1));
+  }
+  auto read_x = [&](Frags& F, uint32_t slot, int h, int t, int e) {
+    F.x[t][e] = *reinterpret_cast<const u32x4_t*>(lds + (slot + wt * 128) + xpos[h][e] + 4096 * t);
+  };
+  auto read_w = [&](Frags& F, uint32_t slot, int h, int f, int e) {
+    if (DX) {
+#pragma unroll
+      for (int q = 2 * e; q < 2 * e + 2; ++q) {
+        const v2i_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i_t*)((lds_u8_t*)lds + slot + wpos[f] + WF * (64 * h + 8 * q)));
+        F.w[f][e][2 * (q & 1)] = (uint32_t)v[0];
+        F.w[f][e][2 * (q & 1) + 1] = (uint32_t)v[1];
       }
+    } else {
+      F.w[f][e] = *reinterpret_cast<const u32x4_t*>(lds + (slot + wf * 128) + xpos[h][e] + 4096 * f);
+    }
+  };
+  // read n (0 .. NR - 1) of a step's fragments, in the order the MFMAs need them
+  auto read = [&](Frags& F, uint32_t xslot, uint32_t wslot, int h, int n) {
+    if (n < 2) read_w(F, wslot, h, 0, n);
+    else if (n < 2 + 2 * S) read_x(F, xslot, h, (n - 2) >> 1, n & 1);
+    else read_w(F, wslot, h, (n - 2 * S) >> 1, n & 1);
+  };
+
+  f32x16_t acc[S][S];  // [feature tile][token tile]
+#pragma unroll
+  for (int f = 0; f < S; ++f)
+#pragma unroll
+    for (int t = 0; t < S; ++t)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[f][t][v] = 0.0f;
+
+  uint32_t sx[S], sxn[S], swc;
+  u32x4_t sxq[S];
+  SwRaw swn;
+  Frags F[2];
+#pragma unroll
+  for (int t = 0; t < S; ++t) {
+    if (DX) {
+      sxq[t] = load_sx4(0, t);
+      sx[t] = sxq[t][0];
+    } else {
+      sx[t] = sxn[t] = load_sx(0, t);
+    }
+  }
+  swn = load_sw(0);
+  swc = sw_of(swn);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) copy_x(c, 2 * c * kSlot, j);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) copy_w(c, (2 * c + 1) * kSlot, j);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  dma::wait_vm<2 * NC>();  // the first pair's copies have landed; the second's went out after them
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int n = 0; n < NR; ++n) read(F[0], 0, kSlot, 0, n);
+
+  uint32_t slot = 0;  // X of the step's pair; W's is the next one
+  // step u, J = u % 8; in_loop: the loads of the next group's scales are there
+  // to be counted (behind the loop nothing uses them, and they are gone)
+  auto step = [&](uint32_t u, auto j_, auto in_loop_) {
+    constexpr int J = decltype(j_)::value, Q = J / 2;
+    constexpr bool loads = decltype(in_loop_)::value && !DX;
+    constexpr bool odd = J % 2 != 0;
+    Frags& C = F[odd];
+    Frags& Nx = F[!odd];
+    const uint32_t pr = u / 2;
+    // the next step's fragments: the pair's second half, or the next pair's first
+    const uint32_t rx_ = odd ? slot_after(slot, 2) : slot, rw_ = odd ? slot_after(slot, 3) : slot_after(slot, 1);
+    const uint32_t fill = odd ? slot : slot_after(slot, 4);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int f = m / S, t = m % S;
+      const u32x4_t w0 = C.w[f][0], w1 = C.w[f][1], x0 = C.x[t][0], x1 = C.x[t][1];
+      acc[f][t] = mfma8<Q>(v8i_t{(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]},
+                           v8i_t{(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]},
+                           acc[f][t], swc, sx[t]);
+      // what goes out behind this MFMA: its share of the next step's reads and of the copies
+      constexpr int first = odd ? BAR + 1 : 0;
+      if (odd && m == BAR) {
+        // the next pair's copies have landed (after them went out those of X
+        // in the step before, and the scales' loads if that was J = 2), and
+        // this wave's fragments of the pair are read
+        dma::wait_vm<loads && J == 3 ? NC + S : NC>();
+        lds_barrier();
+      }
+      if (m >= first) {
+#pragma unroll
+        for (int n = NR * (m - first) / (M - first); n < NR * (m + 1 - first) / (M - first); ++n)
+          read(Nx, rx_, rw_, odd ? 0 : 1, n);
+#pragma unroll
+        for (int n = NC * (m - first) / (M - first); n < NC * (m + 1 - first) / (M - first); ++n) {
+          if (odd) copy_w(pr + 2, fill, n);
+          else copy_x(pr + 2, fill, n);
+        }
+      }
+      if (loads && J == 2 && m % S == 1) sxn[m / S] = load_sx(u / 8 + 1, m / S);
+      if (J == 2 && m == M / 2) swn = load_sw(u / 8 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (odd) slot = slot_after(slot, 2);
+  };
+  auto steps8 = [&](uint32_t u) {
+    step(u, std::integral_constant<int, 0>(), std::true_type());
+    step(u + 1, std::integral_constant<int, 1>(), std::true_type());
+    step(u + 2, std::integral_constant<int, 2>(), std::true_type());
+    step(u + 3, std::integral_constant<int, 3>(), std::true_type());
+    step(u + 4, std::integral_constant<int, 4>(), std::true_type());
+    step(u + 5, std::integral_constant<int, 5>(), std::true_type());
+    step(u + 6, std::integral_constant<int, 6>(), std::true_type());
+    step(u + 7, std::integral_constant<int, 7>(), std::true_type());
+    swc = sw_of(swn);
+  };
+  uint32_t u = 0;
+  if (DX) {
+    for (uint32_t quad = 1; u + 8 <= nsteps; ++quad) {
+      u32x4_t nq[S];
+#pragma unroll
+      for (int t = 0; t < S; ++t) nq[t] = load_sx4(quad, t);  // past the row's end: not used
+      for (int k = 1; k <= 4 && u + 8 <= nsteps; ++k, u += 8) {
+        steps8(u);
+#pragma unroll
+        for (int t = 0; t < S; ++t) sx[t] = k == 1 ? sxq[t][1] : k == 2 ? sxq[t][2] : sxq[t][3];
+      }
+#pragma unroll
+      for (int t = 0; t < S; ++t) sxq[t] = nq[t];
+      if (u % 32 == 0) {
+#pragma unroll
+        for (int t = 0; t < S; ++t) sx[t] = sxq[t][0];
+      }
+    }
+  } else {
+    for (; u + 8 <= nsteps; u += 8) {
+      steps8(u);
+#pragma unroll
+      for (int t = 0; t < S; ++t) sx[t] = sxn[t];
+    }
+  }
+  if (u < nsteps) step(u, std::integral_constant<int, 0>(), std::false_type());
+  if (u + 1 < nsteps) step(u + 1, std::integral_constant<int, 1>(), std::false_type());
+  if (u + 2 < nsteps) step(u + 2, std::integral_constant<int, 2>(), std::false_type());
+  if (u + 3 < nsteps) step(u + 3, std::integral_constant<int, 3>(), std::false_type());
+  if (u + 4 < nsteps) step(u + 4, std::integral_constant<int, 4>(), std::false_type());
+  if (u + 5 < nsteps) step(u + 5, std::integral_constant<int, 5>(), std::false_type());
+  if (u + 6 < nsteps) step(u + 6, std::integral_constant<int, 6>(), std::false_type());
+
+  // (lane numbers formed anew: what is derived from them here need not live
+  // through the loop, whose registers are all taken)
+  int le = lane;
+  asm volatile("" : "+v"(le));
+  const int ge = le >> 5, ce = le & 31;
+  if (p.r > 0 && split == 0) {
+    // the next sixteen columns' fragments are loaded while one's multiply
+    bf16x8_t wa[2][S], xb[2][S];
+    auto load = [&](int c0, bf16x8_t(&w)[S], bf16x8_t(&x)[S]) {
+#pragma unroll
+      for (int f = 0; f < S; ++f) w[f] = tail_weight(p, f0 + wf + 32 * f + ce, feats, c0 + 8 * ge);
+#pragma unroll
+      for (int t = 0; t < S; ++t) x[t] = tail_token(p, t0 + wt + 32 * t + ce, c0 + 8 * ge);
+    };
+    auto mul = [&](const bf16x8_t(&w)[S], const bf16x8_t(&x)[S]) {
+#pragma unroll
+      for (int f = 0; f < S; ++f)
+#pragma unroll
+        for (int t = 0; t < S; ++t)
+          acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[f], x[t], acc[f][t], 0, 0, 0);
+    };
+    load(0, wa[0], xb[0]);
+    for (int c0 = 0; c0 < 2 * p.r; c0 += 32) {  // columns up to ldh, a multiple of 64, are there
+      load(c0 + 16, wa[1], xb[1]);
+      mul(wa[0], xb[0]);
+      if (c0 + 32 < 2 * p.r) load(c0 + 32, wa[0], xb[0]);
+      mul(wa[1], xb[1]);
     }
   }
 
   if (L.nsplit > 1) {
+    dma::wait_vm<0>();  // no copy may land in LDS that is no longer this workgroup's
     float* part = p.part + (int64_t)split * p.T * feats;
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int t = 0; t < S; ++t) {
+      const int64_t tok = t0 + wt + 32 * t + ce;
+      if (tok >= p.T) continue;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t t = t0 + wt + 16 * c + i, f = f0 + wf + 16 * a + 4 * g;
-        if (t < p.T && f < feats) *reinterpret_cast<f32x4_t*>(part + t * feats + f) = acc[a][c];
-      }
+      for (int f = 0; f < S; ++f)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          const int64_t col = f0 + wf + 32 * f + 2 * v + 4 * ge;
+          if (col < feats)
+            *reinterpret_cast<f32x4_t*>(part + tok * feats + col) =
+                f32x4_t{acc[f][t][v], acc[f][t][v + 1], acc[f][t][v + 2], acc[f][t][v + 3]};
+        }
+    }
     return;
   }
+
+  // every wave's copies have landed and every fragment is read before the
+  // output tile goes over the stages
+  dma::wait_vm<0>();
   __syncthreads();
-  uint16_t* out = reinterpret_cast<uint16_t*>(lds);  // [token][feature]
+  // lane l, value v: token 32 t + l % 32, feature 8 (v / 4) + 4 (l / 32) + v % 4
+  uint16_t* out = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int f = 0; f < S; ++f)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f32x4_t v = acc[a][c];
-      *reinterpret_cast<uint2*>(out + (wt + 16 * c + i) * kOutLd + wf + 16 * a + 4 * g) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    }
+    for (int t = 0; t < S; ++t)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4)
+        *reinterpret_cast<uint2*>(out + (wt + 32 * t + ce) * kOutLd + wf + 32 * f + 2 * v + 4 * ge) =
+            make_uint2(pack_bf16x2(acc[f][t][v], acc[f][t][v + 1]), pack_bf16x2(acc[f][t][v + 2], acc[f][t][v + 3]));
   __syncthreads();
-  for (int e = threadIdx.x; e < BT * BT / 8; e += 256) {
-    const int R = e >> 4, col = (e & 15) * 8;
+  for (int e = threadIdx.x; e < WT * WF / 8; e += 256) {
+    const int R = e / (WF / 8), col = e % (WF / 8) * 8;
     if (t0 + R < p.T && f0 + col < feats)
-      *reinterpret_cast<u32x4_t*>(p.C + (t0 + R) * feats + f0 + col) =
-          *reinterpret_cast<const u32x4_t*>(out + R * kOutLd + col);
+      *reinterpret_cast<u32x4_t*>(p.C + (t0 + R) * feats + f0 + col) = *reinterpret_cast<const u32x4_t*>(out + R * kOutLd + col);
   }
 }
-static_assert(BT * kOutLd * 2 <= 4 * kTileBytes, "the output tile fits over the stages");
 
+__global__ __launch_bounds__(256, 1) void k_fp8_wide_256(WideLaunch L) { product<false, 4>(L); }
+__global__ __launch_bounds__(256, 1) void k_fp8_wide_256_dx(WideLaunch L) { product<true, 4>(L); }
+__global__ __launch_bounds__(256, 2) void k_fp8_wide_128(WideLaunch L) { product<false, 2>(L); }
+__global__ __launch_bounds__(256, 2) void k_fp8_wide_128_dx(WideLaunch L) { product<true, 2>(L); }
+
+}  // namespace
+
+namespace {
 // The contraction ranges' partial sums in range order, rounded once; four
 // consecutive elements a thread.
 __global__ __launch_bounds__(256) void k_fp8_sum(const float* __restrict__ part, int nsplit, int64_t n,
                                                  uint16_t* __restrict__ C) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= n) return;
-  float4 v = *reinterpret_cast<const float4*>(part + e);
-  for (int q = 1; q < nsplit; ++q) {
-    const float4 w = *reinterpret_cast<const float4*>(part + q * n + e);
-    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-  }
-  *reinterpret_cast<uint2*>(C + e) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(part + e);
+  for (int q = 1; q < nsplit; ++q) v += *reinterpret_cast<const f32x4_t*>(part + q * n + e);
+  *reinterpret_cast<uint2*>(C + e) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-__global__ __launch_bounds__(256) void k_fp8_pair(const uint16_t* __restrict__ M, int64_t rows, int r, int64_t ldh,
-                                                  int transposed, uint16_t* __restrict__ out) {
-  // 64 rows a workgroup; A's transpose goes through LDS so that both sides are
-  // read and written along their rows
-  __shared__ uint16_t t[64][130];
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int n = (int)(rows - r0 < 64 ? rows - r0 : 64);
-  for (int e = threadIdx.x; e < 64 * r; e += 256) {
-    if (transposed) {
-      const int j = e >> 6, m = e & 63;
-      if (m < n) t[m][j] = M[(int64_t)j * rows + r0 + m];
-    } else {
-      const int m = e / r, j = e - m * r;
-      if (m < n) t[m][j] = M[(r0 + m) * r + j];
+// How a product is cut: the first `wide` features on 256 x 256 tiles, the
+// others on 128 x 128 ones, or all of them on those over nsplit contraction
+// ranges (a multiple of eight steps each) whose sums a second launch adds.
+//
+// Times measured at contractions of 4096 to 11008, in microseconds for n steps
+// of 64: a full round of 256 large tiles (one a CU) 0.72 n + 4, one of w tiles
+// (0.47 + 0.25 w / 256) n + 3; a round of small ones 0.46 n + 3 for 257 to 512
+// (two a CU), 0.29 n + 3 for fewer; a further launch 5; a pass over partial sums
+// 3 and their bytes, written and read, at 4 TB/s.  So a large tile is done 1.3
+// times as fast for its size where rounds are full (4096 x 8192 x 8192: 185 us
+// against 234), and the small ones win where they would not be (1333 x 4096 x
+// 4096: 31 against 39).
+struct ProductPlan {
+  int64_t wide;
+  int32_t nsplit;
+  uint32_t split_steps;
+};
+
+double large_time(int64_t tiles, int64_t steps) {
+  const int64_t rest = tiles % 256;
+  return (double)(tiles / 256) * (0.72 * steps + 4) + (rest ? (0.47 + 0.25 * rest / 256) * steps + 3 : 0.0);
+}
+double small_time(int64_t tiles, int64_t steps) {
+  const int64_t rest = tiles % 512;
+  return (double)(tiles / 512) * (0.46 * steps + 3) + (rest ? (rest > 256 ? 0.46 : 0.29) * steps + 3 : 0.0);
+}
+
+ProductPlan plan_product(int64_t T, int64_t feats, int64_t len) {
+  const int64_t steps = len / 64, groups = (steps + 7) / 8;
+  const int64_t mt4 = (T + 255) / 256, nt4 = (feats + 255) / 256, mt2 = (T + 127) / 128;
+  const auto small_tiles = [&](int64_t f) { return mt2 * ((f + 127) / 128); };
+  ProductPlan best{0, 1, (uint32_t)(groups * 8)};
+  double time = small_time(small_tiles(feats), steps);
+  // whole rounds of large tiles, the last features on small ones; or large tiles alone
+  for (int64_t rounds = 1;; ++rounds) {
+    const int64_t cols = rounds * 256 / mt4 < nt4 ? rounds * 256 / mt4 : nt4;
+    if (cols > 0) {
+      const int64_t wide = cols * 256 < feats ? cols * 256 : feats;
+      const double t = large_time(cols * mt4, steps) + (wide < feats ? 5 + small_time(small_tiles(feats - wide), steps) : 0.0);
+      if (t < time) {
+        time = t;
+        best.wide = wide;
+      }
+    }
+    if (cols == nt4) break;
+  }
+  for (int64_t s = 2; s <= 16 && s <= groups; ++s) {
+    const int64_t per = (groups + s - 1) / s;
+    if ((groups + per - 1) / per != s) continue;  // an empty range
+    const double t = small_time(small_tiles(feats) * s, per * 8) + 3 + (double)(8 * s) * T * feats / 4e6;
+    if (t < time) {
+      time = t;
+      best = ProductPlan{0, (int32_t)s, (uint32_t)(per * 8)};
     }
   }
-  __syncthreads();
-  const int l = (int)ldh;
-  for (int e = threadIdx.x; e < n * l; e += 256) {
-    const int m = e / l, c = e - m * l;
-    out[(r0 + m) * ldh + c] = c < r ? t[m][c] : (c < 2 * r ? t[m][c - r] : (uint16_t)0);
-  }
+  return best;
 }
 
-// contraction ranges: as many workgroups as fill the 256 CUs twice, each range at least four steps
-int product_splits(int64_t T, int64_t feats, int64_t len) {
-  const int64_t tiles = ((T + BT - 1) / BT) * ((feats + BT - 1) / BT);
-  const int64_t steps = (len + 127) / 128;
-  int64_t s = 512 / tiles;
-  if (s > steps / 4) s = steps / 4;
-  if (s > 16) s = 16;
-  return (int)(s < 1 ? 1 : s);
+template <int S>
+hipError_t launch_tiles(const Fp8Params& p, int64_t f_begin, int64_t f_end, const ProductPlan& plan, hipStream_t stream) {
+  if (f_begin >= f_end) return hipSuccess;
+  WideLaunch L{};
+  L.p = p;
+  L.mt = (int32_t)((p.T + 64 * S - 1) / (64 * S));
+  L.nt = (int32_t)((f_end - f_begin + 64 * S - 1) / (64 * S));
+  L.group = 4;
+  L.f_begin = (int32_t)f_begin;
+  L.nsplit = plan.nsplit;
+  L.split_steps = plan.split_steps;
+  const int64_t tiles = (int64_t)L.mt * L.nt * L.nsplit;
+  KernelEvents ev(KID_FP8_GEMM);
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
+  const auto k = S == 4 ? (p.dx ? k_fp8_wide_256_dx : k_fp8_wide_256) : (p.dx ? k_fp8_wide_128_dx : k_fp8_wide_128);
+  hipExtLaunchKernelGGL(k, grid, dim3(256), 0, stream, ev.start(), ev.stop(), 0, L);
+  return hipGetLastError();
 }
-
 }  // namespace
 
 size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx) {
   const int64_t feats = dx ? Kw : Nw;
-  const int s = product_splits(T, feats, dx ? Nw : Kw);
-  return s > 1 ? (size_t)s * T * feats * 4 : 0;
+  const ProductPlan plan = plan_product(T, feats, dx ? Nw : Kw);
+  return plan.nsplit > 1 ? (size_t)plan.nsplit * T * feats * 4 : 0;
 }
 
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
-  if (((p.T + 255) / 256) * (((p.dx ? p.Kw : p.Nw) + 255) / 256) >= 128) return launch_fp8_wide(p, stream);
-  Fp8Launch L{};
-  L.p = p;
-  const int64_t feats = p.dx ? p.Kw : p.Nw, len = p.dx ? p.Nw : p.Kw;
-  L.out_cols = feats;
-  L.mt = (int32_t)((feats + BT - 1) / BT);
-  L.nt = (int32_t)((p.T + BT - 1) / BT);
-  L.steps = (int32_t)((len + 127) / 128);
-  L.nsplit = product_splits(p.T, feats, len);
-  L.steps_per_split = (L.steps + L.nsplit - 1) / L.nsplit;
-  if (L.nsplit > 1 && (!p.part || p.part_bytes < fp8_product_part_bytes(p.T, p.Nw, p.Kw, p.dx)))
+  const int64_t feats = p.dx ? p.Kw : p.Nw;
+  const ProductPlan plan = plan_product(p.T, feats, p.dx ? p.Nw : p.Kw);
+  if (plan.nsplit > 1 && (!p.part || p.part_bytes < fp8_product_part_bytes(p.T, p.Nw, p.Kw, p.dx)))
     return hipErrorInvalidValue;
-  {
-    KernelEvents ev(KID_FP8_GEMM);
-    const hipEvent_t e0 = ev.start(), e1 = ev.stop();
-    const dim3 grid((unsigned)(L.mt * L.nt * L.nsplit));
-    if (p.dx) hipExtLaunchKernelGGL(k_fp8_tile<true>, grid, dim3(256), 0, stream, e0, e1, 0, L);
-    else hipExtLaunchKernelGGL(k_fp8_tile<false>, grid, dim3(256), 0, stream, e0, e1, 0, L);
-  }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || L.nsplit == 1) return e;
+  hipError_t e = launch_tiles<4>(p, 0, plan.wide, plan, stream);
+  if (e == hipSuccess) e = launch_tiles<2>(p, plan.wide, feats, plan, stream);
+  if (e != hipSuccess || plan.nsplit == 1) return e;
   const int64_t n = p.T * feats;
   KernelEvents ev(KID_REDUCE);
   hipExtLaunchKernelGGL(k_fp8_sum, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream, ev.start(), ev.stop(),
-                        0, p.part, L.nsplit, n, p.C);
+                        0, p.part, plan.nsplit, n, p.C);
   return hipGetLastError();
 }
+
+namespace {
+// 64 rows and 32 columns j of the source a workgroup; A's transpose goes
+// through LDS so that both sides are read and written along their rows.
+__global__ __launch_bounds__(256) void k_fp8_pair(const uint16_t* __restrict__ M, int64_t rows, int r, int64_t ldh,
+                                                  int transposed, uint16_t* __restrict__ out) {
+  __shared__ uint16_t t[64][34];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int j0 = (int)blockIdx.y * 32;
+  const int n = (int)(rows - r0 < 64 ? rows - r0 : 64);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int e = threadIdx.x + 256 * q;
+    const int m = transposed ? e & 63 : e >> 5, j = transposed ? e >> 6 : e & 31;
+    uint16_t v = 0;
+    if (m < n && j0 + j < r) v = transposed ? M[(int64_t)(j0 + j) * rows + r0 + m] : M[(r0 + m) * r + j0 + j];
+    t[m][j] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int e = threadIdx.x + 256 * q;
+    const int m = e >> 5, j = j0 + (e & 31);
+    if (m >= n) continue;
+    uint16_t* row = out + (r0 + m) * ldh;
+    if (j < r) {
+      row[j] = t[m][e & 31];
+      row[r + j] = t[m][e & 31];
+    }
+    // the padding behind the pair, shared out among the columns
+    for (int64_t c = 2 * r + j; c < ldh; c += 32 * gridDim.y) row[c] = 0;
+  }
+}
+}  // namespace
 
 hipError_t launch_fp8_pair(const uint16_t* M, int64_t rows, int r, int64_t ldh, int transposed, uint16_t* out,
                            hipStream_t stream) {
   KernelEvents ev(KID_FP8_DOWN);
-  hipExtLaunchKernelGGL(k_fp8_pair, dim3((unsigned)((rows + 63) / 64)), dim3(256), 0, stream, ev.start(), ev.stop(), 0,
+  hipExtLaunchKernelGGL(k_fp8_pair, dim3((unsigned)((rows + 63) / 64), (unsigned)((r + 31) / 32)), dim3(256), 0, stream, ev.start(), ev.stop(), 0,
                         M, rows, r, ldh, transposed, out);
   return hipGetLastError();
 }

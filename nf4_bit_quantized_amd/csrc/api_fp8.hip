@@ -45,8 +45,8 @@ Fp8FwdWs plan_fwd(int64_t N, int64_t K, int64_t T, int32_t r, void* ws) {
   Fp8FwdWs w;
   Carve c(ws);
   if (T > 0) {
-    w.part_bytes = fp8_product_part_bytes(T, N, K, 0);
-    if (r > 0) {
+    w.part_bytes = fp8_product_part_bytes(T, N, K, 0, r);
+    if (r > 0 && T > kFp8FewT) {
       w.U = static_cast<float*>(c.take((size_t)T * r * 4));
       w.Us = static_cast<uint16_t*>(c.take((size_t)T * hilo_ld(r) * 2));
       if (r % 8 != 0) w.Bp = static_cast<uint16_t*>(c.take((size_t)N * hilo_ld(r) * 2));
@@ -76,12 +76,12 @@ Fp8BwdWs plan_bwd(int64_t N, int64_t K, int64_t T, int32_t r, void* ws) {
   if (T > 0) {
     w.dYc = static_cast<uint8_t*>(c.take((size_t)(T * N)));
     w.dYs = static_cast<uint8_t*>(c.take((size_t)(T * fp8_scale_ld(N))));
-    w.part_bytes = fp8_product_part_bytes(T, N, K, 1);
+    w.part_bytes = fp8_product_part_bytes(T, N, K, 1, r);
     if (r > 0) {
       w.G = static_cast<float*>(c.take((size_t)T * r * 4));
       w.U = static_cast<float*>(c.take((size_t)T * r * 4));
       w.Gs = static_cast<uint16_t*>(c.take((size_t)T * hilo_ld(r) * 2));
-      w.Ap = static_cast<uint16_t*>(c.take((size_t)K * hilo_ld(r) * 2));
+      if (T > kFp8FewT) w.Ap = static_cast<uint16_t*>(c.take((size_t)K * hilo_ld(r) * 2));
       w.part_bytes = std::max(std::max(w.part_bytes, fp8_down_part_bytes(T, K, r)),
                               std::max(lora_g_part_bytes(T, N, r), fp8_grad_part_bytes(T, K, N, r)));
     }
@@ -154,9 +154,11 @@ int qlora_fp8_linear_fwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
   P.X = X_codes; P.Xs = X_scales; P.W = W_codes; P.Ws = W_scales;
   P.T = T; P.Nw = N; P.Kw = K; P.dx = 0; P.r = r; P.ldh = hilo_ld(r);
   P.C = Y; P.part = w.part; P.part_bytes = w.part_bytes;
-  if (r > 0) {
-    const float s = alpha / (float)r;
-    const Fp8DownParams Dn{X_codes, X_scales, A, T, K, r, s, U_out ? U_out : w.U, w.Us, P.ldh, w.part, w.part_bytes};
+  if (r > 0) P.s = alpha / (float)r;
+  if (r > 0 && T <= kFp8FewT) {
+    P.A = A; P.M = B; P.U = U_out;
+  } else if (r > 0) {
+    const Fp8DownParams Dn{X_codes, X_scales, A, T, K, r, P.s, U_out ? U_out : w.U, w.Us, P.ldh, w.part, w.part_bytes};
     HIP_TRY(launch_fp8_down(Dn, s_));
     P.At = w.Us;
     P.Bt = B;
@@ -220,7 +222,9 @@ int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
     P.X = w.dYc; P.Xs = w.dYs; P.W = W_codes; P.Ws = W_scales;
     P.T = T; P.Nw = N; P.Kw = K; P.dx = 1; P.r = r; P.ldh = ldh;
     P.C = dX; P.part = w.part; P.part_bytes = w.part_bytes;
-    if (r > 0) {
+    if (r > 0 && T <= kFp8FewT) {
+      P.s = s; P.M = A; P.G = w.G;
+    } else if (r > 0) {
       HIP_TRY(launch_fp8_pair(A, K, r, ldh, 1, w.Ap, s_));
       P.At = w.Gs; P.Bt = w.Ap; P.bt_pair = 1;
     }

@@ -36,10 +36,18 @@ struct Fp8Params {
   const uint16_t* Bt;  // bt_pair == 0: B [rows][r], r % 8 == 0; 1: [rows][ldh] (the pair operand)
   int32_t bt_pair;
   uint16_t* C;
-  float* part;         // contraction-split partial sums, fp8_product_part_bytes
+  float* part;         // partial sums, fp8_product_part_bytes
   size_t part_bytes;
+  // at most kFp8FewT tokens and r > 0: the rank-r term comes from these instead
+  // of from At and Bt, and the forward's U is formed by the product's own launch
+  float s;
+  const uint16_t* A;   // forward: bf16 [r][Kw]
+  const uint16_t* M;   // forward: B [Nw][r]; dx: A [r][Kw]
+  const float* G;      // dx: fp32 [T][r]
+  float* U;            // forward: receives U, or null
 };
-size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx);
+constexpr int64_t kFp8FewT = 128;
+size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx, int r);
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream);
 
 // The pair operand of a tail: out [rows][ldh] = (V | V | 0), V [rows][r] being

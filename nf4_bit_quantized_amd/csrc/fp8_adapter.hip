@@ -8,38 +8,28 @@
 // accuracy, where a pair of terms would round them to about 17 bits.
 #include "dma.hpp"
 #include "fp8.hpp"
+#include "fp8_down.hpp"
 #include "lds_tr.hpp"
 #include "trace.hpp"
 
 namespace qlora {
 namespace {
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+using fp8::down_tile;
+using fp8::mfma16;
+using fp8::restore8;
+using fp8::scale_of;
+using fp8::u32x4_t;
 using ldstr::tr_frag_swz;
 using ldstr::tr_swz;
 
-__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
-
-// Eight codes (two dwords) restored: exact, save below bf16's own range.
-__device__ __forceinline__ u32x4_t restore8(uint32_t a, uint32_t b, float k) {
-  return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, true)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, k, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, k, true))};
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf(const void* p, int64_t bytes) {
+  const int32_t n = bytes > 0x7FFFFFF0LL ? 0x7FFFFFF0 : (int32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, 0x00020000);
 }
 
 // ---------------------------------------------------------------------------
-// down
-//
-// A workgroup owns 16 RT tokens and 16 JT columns of U for one range of the
-// contraction; its NW waves take the range's chunks of 128 in turn and add
-// their tiles in LDS in wave order.  Fragments come straight from global
-// memory: lane l of token row l % 16 takes the 32 codes 32 (l/16) .. +31 of
-// the chunk, which are its share of four MFMAs.
+// down: the tile is formed by down_tile (fp8_down.hpp)
 // ---------------------------------------------------------------------------
 struct DownLaunch {
   Fp8DownParams p;
@@ -61,79 +51,22 @@ __device__ __forceinline__ void down_out(const Fp8DownParams& p, int64_t t, int 
   if (p.Us) p.Us[t * p.ldh + c] = h;
 }
 
+// A workgroup owns 16 RT tokens and 16 JT columns of U for one range of the
+// contraction; its NW waves take the range's chunks in turn and add their tiles
+// in LDS in wave order.
 template <int RT, int JT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_fp8_down(DownLaunch L) {
   constexpr int TOK = 16 * RT, COL = 16 * JT, LD = COL + 1;
   __shared__ float red[NW][TOK][LD];
   const Fp8DownParams& p = L.p;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int i = lane & 15, g = lane >> 4;
   int b = (int)blockIdx.x;
   const int split = b / (L.ttiles * L.jtiles);
   b -= split * (L.ttiles * L.jtiles);
   const int64_t t0 = (int64_t)(b / L.jtiles) * TOK;
   const int j0 = (b % L.jtiles) * COL;
-  const int64_t ldx = fp8_scale_ld(p.K);
   const int c_begin = split * L.chunks_per_split;
   const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
-
-  f32x4_t acc[RT][JT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int jt = 0; jt < JT; ++jt) acc[rt][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  // rows past the end repeat the last one; their sums are never stored
-  const uint8_t* xrow[RT];
-  const uint8_t* srow[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int64_t t = t0 + 16 * rt + i < p.T ? t0 + 16 * rt + i : p.T - 1;
-    xrow[rt] = p.X + t * p.K;
-    srow[rt] = p.Xs + t * ldx;
-  }
-  const uint16_t* arow[JT];
-#pragma unroll
-  for (int jt = 0; jt < JT; ++jt) {
-    const int j = j0 + 16 * jt + i < p.r ? j0 + 16 * jt + i : p.r - 1;
-    arow[jt] = p.A + (int64_t)j * p.K;
-  }
-  for (int ch = c_begin + wave; ch < c_end; ch += NW) {
-    const int64_t k = (int64_t)ch * 128 + 32 * g;
-    const bool in = k < p.K;  // the last chunk of a row may be half a chunk
-    u32x4_t x[RT][2];
-    float sc[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      sc[rt] = scale_of(srow[rt][ch]);
-      const u32x4_t* src = reinterpret_cast<const u32x4_t*>(xrow[rt] + (in ? k : 0));
-      x[rt][0] = src[0];
-      x[rt][1] = src[1];
-      if (!in) x[rt][0] = x[rt][1] = u32x4_t{0u, 0u, 0u, 0u};
-    }
-#pragma unroll
-    for (int jt = 0; jt < JT; ++jt) {
-      const u32x4_t* src = reinterpret_cast<const u32x4_t*>(arow[jt] + (in ? k : 0));
-      u32x4_t a[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) a[q] = in ? src[q] : u32x4_t{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const u32x4_t v = restore8(x[rt][q >> 1][2 * (q & 1)], x[rt][q >> 1][2 * (q & 1) + 1], sc[rt]);
-          acc[rt][jt] = mfma16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, a[q]), acc[rt][jt]);
-        }
-    }
-  }
-  // lane l, value v: token 16 rt + 4 (l/16) + v, column 16 jt + l % 16
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int jt = 0; jt < JT; ++jt)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][16 * rt + 4 * g + v][16 * jt + i] = acc[rt][jt][v];
+  down_tile<RT, JT, NW, LD>(p, t0, j0, c_begin, c_end, __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), red);
   __syncthreads();
   auto sum = [&](int rr, int j) {
     float v = red[0][rr][j];
@@ -212,20 +145,16 @@ struct GradLaunch {
   int32_t nsplit, chunks, chunks_per_split;
 };
 
-template <int JT>
-__global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
+// second: dB, over bf16 rows; else dA, over codes.
+template <int JT, bool second>
+__device__ __forceinline__ void grad_body(const GradLaunch& L, int slab, int split,
+                                          uint16_t (*lds)[kGradChunk * (kGradM + 48 * JT)]) {
   constexpr int QLD = 16 * JT;
   constexpr int kP = kGradChunk * kGradM, kQ = kGradChunk * QLD;  // elements
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][kP + 3 * kQ];
   const Fp8GradParams& p = L.p;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int i = lane & 15, g = lane >> 4;
-  const int slabs = L.slabs_a + L.slabs_b;
-  const int split = (int)blockIdx.x / slabs;
-  int slab = (int)blockIdx.x - split * slabs;
-  const bool second = slab >= L.slabs_a;  // dB
-  if (second) slab -= L.slabs_a;
   const int64_t m0 = (int64_t)slab * kGradM;
   const int64_t D = second ? p.N : p.K;
   const float* Q = second ? p.U : p.G;
@@ -237,36 +166,35 @@ __global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
   // thread: row tid / 16 of the chunk, 16 columns of P and JT of Q
   const int row = threadIdx.x >> 4, pc = threadIdx.x & 15;
   const int64_t col = m0 + 16 * pc;
-  u32x4_t pw[2];
-  uint32_t ps = 127;
-  float qv[JT];
-  auto fetch = [&](int ch) {
-    const int64_t t = (int64_t)ch * kGradChunk + row;
-    const bool in = t < p.T && col < D;
-    pw[0] = pw[1] = u32x4_t{0u, 0u, 0u, 0u};
-    if (in) {
-      if (second) {
-        const u32x4_t* src = reinterpret_cast<const u32x4_t*>(p.dY + t * p.N + col);
-        pw[0] = src[0];
-        pw[1] = src[1];
-      } else {
-        pw[0] = *reinterpret_cast<const u32x4_t*>(p.X + t * p.K + col);
-        ps = p.Xs[t * ldx + (col >> 7)];
-      }
-    }
+  struct Chunk {
+    u32x4_t p[second ? 2 : 1];
+    uint32_t s;
+    float q[JT];
+  };
+  // (buffer loads: what lies outside reads zero, with nothing to wait for)
+  const __amdgpu_buffer_rsrc_t rp = second ? buf(p.dY, p.T * p.N * 2) : buf(p.X, p.T * p.K);
+  const __amdgpu_buffer_rsrc_t rs = buf(p.Xs, second ? 0 : p.T * ldx), rq = buf(Q, p.T * r * 4);
+  auto fetch = [&](Chunk& c, int ch) {
+    const uint32_t t = (uint32_t)ch * kGradChunk + row;
+    const bool in = ch < c_end && t < p.T, ok = in && col < D;
+    const uint32_t at = (uint32_t)((t * D + col) * (second ? 2 : 1));
+    c.p[0] = __builtin_amdgcn_raw_buffer_load_b128(rp, ok ? at : dma::kOob, 0, 0);
+    if (second) c.p[second ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(rp, ok ? at + 16 : dma::kOob, 0, 0);
+    else c.s = __builtin_amdgcn_raw_buffer_load_b8(rs, ok ? (uint32_t)(t * ldx + (col >> 7)) : dma::kOob, 0, 0);
 #pragma unroll
     for (int q = 0; q < JT; ++q) {
       const int j = pc + 16 * q;
-      qv[q] = t < p.T && j < r ? Q[t * r + j] : 0.0f;
+      c.q[q] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(rq, in && j < r ? (t * (uint32_t)r + j) * 4u : dma::kOob, 0, 0));
     }
   };
-  auto stage = [&](int buf) {
+  auto stage = [&](const Chunk& c, int buf) {
     uint16_t* P = lds[buf];
-    u32x4_t a = pw[0], b = pw[1];
+    u32x4_t a = c.p[0], b = c.p[second ? 1 : 0];
     if (!second) {
-      const float k = scale_of(ps);
-      b = restore8(pw[0][2], pw[0][3], k);
-      a = restore8(pw[0][0], pw[0][1], k);
+      const float k = scale_of(c.s);
+      b = restore8(c.p[0][2], c.p[0][3], k);
+      a = restore8(c.p[0][0], c.p[0][1], k);
     }
     const int s = tr_swz(row, kGradM / 8);
     *reinterpret_cast<u32x4_t*>(P + row * kGradM + (((2 * pc) ^ s) << 3)) = a;
@@ -275,7 +203,7 @@ __global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
 #pragma unroll
     for (int q = 0; q < JT; ++q) {
       const int j = pc + 16 * q;
-      const float v = p.s * qv[q];
+      const float v = p.s * c.q[q];
       uint16_t h, m, l;
       split_bf16(v, h, m);
       const float rest = v - bf16_bits_to_f32(h);
@@ -293,11 +221,10 @@ __global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) acc[a][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  if (c_begin < c_end) fetch(c_begin);
-  for (int ch = c_begin; ch < c_end; ++ch) {
-    const int buf = (ch - c_begin) & 1;
-    stage(buf);
-    if (ch + 1 < c_end) fetch(ch + 1);
+  Chunk c0, c1;
+  auto body = [&](Chunk& c, int ch, int buf) {
+    stage(c, buf);
+    fetch(c, ch + 2);
     lds_barrier();  // the chunk is staged; every wave is done with the other buffer
     const uint16_t* P = lds[buf];
     bf16x8_t pa[2];
@@ -311,6 +238,12 @@ __global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
 #pragma unroll
         for (int a = 0; a < 2; ++a) acc[a][jt] = mfma16(pa[a], qb, acc[a][jt]);
       }
+  };
+  fetch(c0, c_begin);
+  fetch(c1, c_begin + 1);
+  for (int ch = c_begin; ch < c_end; ch += 2) {
+    body(c0, ch, 0);
+    if (ch + 1 < c_end) body(c1, ch + 1, 1);
   }
 
   // lane l, value v: column m = 32 wave + 16 a + 4 (l/16) + v, j = 16 jt + l % 16
@@ -344,6 +277,15 @@ __global__ __launch_bounds__(512) void k_fp8_grad(GradLaunch L) {
       }
     }
   }
+}
+
+template <int JT>
+__global__ __launch_bounds__(512, JT <= 4 ? 4 : 2) void k_fp8_grad(GradLaunch L) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][kGradChunk * (kGradM + 48 * JT)];
+  const int slabs = L.slabs_a + L.slabs_b;
+  const int split = (int)blockIdx.x / slabs, slab = (int)blockIdx.x - split * slabs;
+  if (slab >= L.slabs_a) grad_body<JT, true>(L, slab - L.slabs_a, split, lds);
+  else grad_body<JT, false>(L, slab, split, lds);
 }
 
 // The token ranges' partial sums in order (dA's, then dB's), four elements a

@@ -47,6 +47,7 @@
 // transposing reads (16 lanes: 8 rows of 16 bytes, a lane receives a column).
 #include "dma.hpp"
 #include "fp8.hpp"
+#include "fp8_down.hpp"
 #include "fp8_tail.hpp"
 #include "trace.hpp"
 
@@ -71,6 +72,7 @@ struct WideLaunch {
   int32_t f_begin;        // the first feature
   int32_t nsplit;         // contraction ranges of a tile
   uint32_t split_steps;   // steps of a range, a multiple of 8
+  int32_t partial;        // the sums go to p.part, [range][T][features]
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf(const void* p, int64_t bytes) {
@@ -97,7 +99,7 @@ __device__ __forceinline__ void copy16_uncounted(dma::v4i_t r, uint32_t voff, ui
 // DX: the weight's contraction runs down its rows; S: 32 x 32 tiles of a wave
 // each way (4: tiles of 256 x 256, a workgroup per CU; 2: 128 x 128, two).
 template <bool DX, int S>
-__device__ __forceinline__ void product(const WideLaunch& L) {
+__device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid, uint8_t* lds) {
   constexpr int WT = 64 * S, WF = 64 * S;       // tokens and features of the tile
   constexpr uint32_t kSlot = WT * 128;
   constexpr int kLds = kSlots * kSlot;
@@ -112,13 +114,12 @@ __device__ __forceinline__ void product(const WideLaunch& L) {
   };
   // the n-th slot after the one at byte o
   auto slot_after = [](uint32_t o, uint32_t n) { return o + n * kSlot < kLds ? o + n * kSlot : o + n * kSlot - kLds; };
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const Fp8Params& p = L.p;
   // runs of consecutive tiles go to one XCD; in their order, groups of token
   // tiles are walked feature tile by feature tile
   const uint32_t mt = (uint32_t)L.mt, nt = (uint32_t)L.nt, gm = (uint32_t)L.group;
   const uint32_t run = (mt * nt * (uint32_t)L.nsplit + 7) / 8;
-  uint32_t order = blockIdx.x % 8 * run + blockIdx.x / 8;
+  uint32_t order = bid % 8 * run + bid / 8;
   if (order >= mt * nt * (uint32_t)L.nsplit) return;
   // the ranges of the contraction follow each other, each over all the tiles
   const uint32_t split = __builtin_amdgcn_readfirstlane(order / (mt * nt));
@@ -145,7 +146,7 @@ __device__ __forceinline__ void product(const WideLaunch& L) {
   const int64_t xbytes = (p.T - t0) * len - k0, wbytes = p.Nw * p.Kw - wbase;
   const __amdgpu_buffer_rsrc_t rx = buf(p.X + xbase, xbytes), rw = buf(p.W + wbase, wbytes);
   const dma::v4i_t ax = dma::rsrc(p.X + xbase, xbytes), aw = dma::rsrc(p.W + wbase, wbytes);  // dx
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(LDS_ADDR(lds));
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8_t*)lds);
   const __amdgpu_buffer_rsrc_t rs = buf(p.Xs, p.T * fp8_scale_ld(len));
 
   // copies of a pair of steps: eight kilobytes of each operand a wave.  Rows
@@ -412,7 +413,7 @@ __device__ __forceinline__ void product(const WideLaunch& L) {
     }
   }
 
-  if (L.nsplit > 1) {
+  if (L.partial) {
     dma::wait_vm<0>();  // no copy may land in LDS that is no longer this workgroup's
     float* part = p.part + (int64_t)split * p.T * feats;
 #pragma unroll
@@ -454,10 +455,142 @@ __device__ __forceinline__ void product(const WideLaunch& L) {
   }
 }
 
-__global__ __launch_bounds__(256, 1) void k_fp8_wide_256(WideLaunch L) { product<false, 4>(L); }
-__global__ __launch_bounds__(256, 1) void k_fp8_wide_256_dx(WideLaunch L) { product<true, 4>(L); }
-__global__ __launch_bounds__(256, 2) void k_fp8_wide_128(WideLaunch L) { product<false, 2>(L); }
-__global__ __launch_bounds__(256, 2) void k_fp8_wide_128_dx(WideLaunch L) { product<true, 2>(L); }
+constexpr int kLds256 = kSlots * 256 * 128, kLds128 = kSlots * 128 * 128;
+
+__global__ __launch_bounds__(256, 1) void k_fp8_wide_256(WideLaunch L) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds256];
+  product<false, 4>(L, blockIdx.x, lds);
+}
+__global__ __launch_bounds__(256, 1) void k_fp8_wide_256_dx(WideLaunch L) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds256];
+  product<true, 4>(L, blockIdx.x, lds);
+}
+__global__ __launch_bounds__(256, 2) void k_fp8_wide_128(WideLaunch L) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds128];
+  product<false, 2>(L, blockIdx.x, lds);
+}
+__global__ __launch_bounds__(256, 2) void k_fp8_wide_128_dx(WideLaunch L) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds128];
+  product<true, 2>(L, blockIdx.x, lds);
+}
+
+// Few tokens.  The product is a stream of the weight, and what costs beside it
+// is launches: U = X A^T runs in the same one, its workgroups first, and the
+// pass that adds the contraction ranges' partial sums also forms the rank-r
+// term from U (or, for dx, from G), in fp32.  One token through 28672 x 8192
+// at r = 64: 49 us against 56 with U and the sums in launches of their own.
+struct FewLaunch {
+  WideLaunch w;
+  Fp8DownParams d;
+  float* upart;  // [uranges][T][r]
+  int32_t jtiles, uranges, uwgs;  // workgroups of U, rounded up to a multiple of eight
+  int32_t chunks, chunks_per_range;
+};
+
+__global__ __launch_bounds__(256, 2) void k_fp8_few(FewLaunch L) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds128];
+  if (blockIdx.x >= (uint32_t)L.uwgs) {
+    product<false, 2>(L.w, blockIdx.x - L.uwgs, lds);
+    return;
+  }
+  const int tiles = (int)((L.d.T + 15) / 16) * L.jtiles;
+  const int range = (int)blockIdx.x / tiles, tile = (int)blockIdx.x - range * tiles;
+  if (range >= L.uranges) return;
+  const int64_t t0 = (int64_t)(tile / L.jtiles) * 16;
+  const int j0 = tile % L.jtiles * 16;
+  const int c_begin = range * L.chunks_per_range;
+  const int c_end = c_begin + L.chunks_per_range < L.chunks ? c_begin + L.chunks_per_range : L.chunks;
+  float(*red)[16][17] = reinterpret_cast<float(*)[16][17]>(lds);
+  fp8::down_tile<1, 1, 4, 17>(L.d, t0, j0, c_begin, c_end, __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), red);
+  __syncthreads();
+  const int rr = threadIdx.x >> 4, j = threadIdx.x & 15;
+  if (t0 + rr < L.d.T && j0 + j < L.d.r)
+    L.upart[((int64_t)range * L.d.T + t0 + rr) * L.d.r + j0 + j] =
+        ((red[0][rr][j] + red[1][rr][j]) + red[2][rr][j]) + red[3][rr][j];
+}
+
+// C[t][f] = bf16( sum over the ranges of part[q][t][f] + s sum_j V[t][j] M ),
+// V being U (its ranges' partial sums added here, and U written) or G, M B[f][j]
+// or, for dx, A[j][f].  A workgroup: kFewT tokens, a feature a thread.
+constexpr int kFewT = 8;
+constexpr int kFewMaxRank = 128;
+
+struct FinishLaunch {
+  const float* part;
+  int32_t nsplit;
+  int64_t T, feats;
+  const float* V;
+  int32_t vranges;
+  int32_t r;
+  float s;
+  const uint16_t* M;
+  float* U;  // forward, or null
+  uint16_t* C;
+};
+
+template <bool DX>
+__global__ __launch_bounds__(256) void k_fp8_finish(FinishLaunch L) {
+  __shared__ float v[kFewT][kFewMaxRank];
+  const int64_t t0 = (int64_t)blockIdx.y * kFewT;
+  const int nt = (int)(L.T - t0 < kFewT ? L.T - t0 : kFewT);
+  const int r = L.r;
+  for (int e = threadIdx.x; e < kFewT * r; e += 256) {
+    const int t = e / r, j = e - t * r;
+    if (t >= nt) {
+      v[t][j] = 0.0f;
+      continue;
+    }
+    float u = L.V[(t0 + t) * r + j];
+    for (int q = 1; q < L.vranges; ++q) u += L.V[((int64_t)q * L.T + t0 + t) * r + j];
+    v[t][j] = L.s * u;
+    if (L.U && blockIdx.x == 0) L.U[(t0 + t) * r + j] = u;
+  }
+  __syncthreads();
+  const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (f >= L.feats) return;
+  // tokens past the last repeat it, and are not stored
+  int64_t row[kFewT];
+  float acc[kFewT];
+#pragma unroll
+  for (int t = 0; t < kFewT; ++t) {
+    row[t] = (t0 + (t < nt ? t : nt - 1)) * L.feats + f;
+    acc[t] = L.part[row[t]];
+  }
+  for (int q = 1; q < L.nsplit; ++q) {
+    const float* src = L.part + (int64_t)q * L.T * L.feats;
+#pragma unroll
+    for (int t = 0; t < kFewT; ++t) acc[t] += src[row[t]];
+  }
+  auto add = [&](int j, float m) {
+#pragma unroll
+    for (int t = 0; t < kFewT; ++t) acc[t] = fmaf(v[t][j], m, acc[t]);
+  };
+  if (DX) {
+    int j = 0;
+    for (; j + 8 <= r; j += 8) {
+      uint16_t m[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m[q] = L.M[(int64_t)(j + q) * L.feats + f];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) add(j + q, bf16_bits_to_f32(m[q]));
+    }
+    for (; j < r; ++j) add(j, bf16_bits_to_f32(L.M[(int64_t)j * L.feats + f]));
+  } else if (r % 8 == 0) {
+    for (int j = 0; j < r; j += 8) {
+      const u32x4_t m = *reinterpret_cast<const u32x4_t*>(L.M + f * r + j);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        add(j + 2 * q, bf16_bits_to_f32(m[q] & 0xFFFFu));
+        add(j + 2 * q + 1, bf16_bits_to_f32(m[q] >> 16));
+      }
+    }
+  } else {
+    for (int j = 0; j < r; ++j) add(j, bf16_bits_to_f32(L.M[f * r + j]));
+  }
+#pragma unroll
+  for (int t = 0; t < kFewT; ++t)
+    if (t < nt) L.C[(t0 + t) * L.feats + f] = f32_to_bf16_bits(acc[t]);
+}
 
 }  // namespace
 
@@ -500,14 +633,14 @@ double small_time(int64_t tiles, int64_t steps) {
   return (double)(tiles / 512) * (0.46 * steps + 3) + (rest ? (rest > 256 ? 0.46 : 0.29) * steps + 3 : 0.0);
 }
 
-ProductPlan plan_product(int64_t T, int64_t feats, int64_t len) {
+ProductPlan plan_product(int64_t T, int64_t feats, int64_t len, bool few) {
   const int64_t steps = len / 64, groups = (steps + 7) / 8;
   const int64_t mt4 = (T + 255) / 256, nt4 = (feats + 255) / 256, mt2 = (T + 127) / 128;
   const auto small_tiles = [&](int64_t f) { return mt2 * ((f + 127) / 128); };
   ProductPlan best{0, 1, (uint32_t)(groups * 8)};
   double time = small_time(small_tiles(feats), steps);
   // whole rounds of large tiles, the last features on small ones; or large tiles alone
-  for (int64_t rounds = 1;; ++rounds) {
+  for (int64_t rounds = 1; !few; ++rounds) {
     const int64_t cols = rounds * 256 / mt4 < nt4 ? rounds * 256 / mt4 : nt4;
     if (cols > 0) {
       const int64_t wide = cols * 256 < feats ? cols * 256 : feats;
@@ -532,8 +665,7 @@ ProductPlan plan_product(int64_t T, int64_t feats, int64_t len) {
 }
 
 template <int S>
-hipError_t launch_tiles(const Fp8Params& p, int64_t f_begin, int64_t f_end, const ProductPlan& plan, hipStream_t stream) {
-  if (f_begin >= f_end) return hipSuccess;
+WideLaunch tiles_launch(const Fp8Params& p, int64_t f_begin, int64_t f_end, const ProductPlan& plan) {
   WideLaunch L{};
   L.p = p;
   L.mt = (int32_t)((p.T + 64 * S - 1) / (64 * S));
@@ -542,6 +674,18 @@ hipError_t launch_tiles(const Fp8Params& p, int64_t f_begin, int64_t f_end, cons
   L.f_begin = (int32_t)f_begin;
   L.nsplit = plan.nsplit;
   L.split_steps = plan.split_steps;
+  L.partial = plan.nsplit > 1;
+  return L;
+}
+
+WideLaunch small_tiles_launch(const Fp8Params& p, const ProductPlan& plan) {
+  return tiles_launch<2>(p, 0, p.dx ? p.Kw : p.Nw, plan);
+}
+
+template <int S>
+hipError_t launch_tiles(const Fp8Params& p, int64_t f_begin, int64_t f_end, const ProductPlan& plan, hipStream_t stream) {
+  if (f_begin >= f_end) return hipSuccess;
+  const WideLaunch L = tiles_launch<S>(p, f_begin, f_end, plan);
   const int64_t tiles = (int64_t)L.mt * L.nt * L.nsplit;
   KernelEvents ev(KID_FP8_GEMM);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8));
@@ -551,17 +695,69 @@ hipError_t launch_tiles(const Fp8Params& p, int64_t f_begin, int64_t f_end, cons
 }
 }  // namespace
 
-size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx) {
+namespace {
+// Few tokens with a rank-r term go through k_fp8_finish, whatever the ranges.
+bool is_few(int64_t T, int r) { return T <= kFp8FewT && r > 0; }
+
+int64_t few_ranges(int64_t T, int64_t K, int r) {
+  // U's ranges: as many as give its tiles 64 workgroups, four chunks each at least
+  const int64_t tiles = (T + 15) / 16 * ((r + 15) / 16), chunks = (K + 127) / 128;
+  int64_t s = (64 + tiles - 1) / tiles;
+  if (s > chunks / 4) s = chunks / 4;
+  if (s < 1) s = 1;
+  const int64_t per = (chunks + s - 1) / s;
+  return (chunks + per - 1) / per;
+}
+}  // namespace
+
+size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx, int r) {
   const int64_t feats = dx ? Kw : Nw;
-  const ProductPlan plan = plan_product(T, feats, dx ? Nw : Kw);
-  return plan.nsplit > 1 ? (size_t)plan.nsplit * T * feats * 4 : 0;
+  const bool few = is_few(T, r);
+  const ProductPlan plan = plan_product(T, feats, dx ? Nw : Kw, few);
+  size_t n = plan.nsplit > 1 || few ? (size_t)plan.nsplit * T * feats * 4 : 0;
+  if (few && !dx) n += (size_t)few_ranges(T, Kw, r) * T * r * 4;
+  return n;
 }
 
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
   const int64_t feats = p.dx ? p.Kw : p.Nw;
-  const ProductPlan plan = plan_product(p.T, feats, p.dx ? p.Nw : p.Kw);
-  if (plan.nsplit > 1 && (!p.part || p.part_bytes < fp8_product_part_bytes(p.T, p.Nw, p.Kw, p.dx)))
-    return hipErrorInvalidValue;
+  const bool few = is_few(p.T, p.r);
+  const ProductPlan plan = plan_product(p.T, feats, p.dx ? p.Nw : p.Kw, few);
+  const size_t need = fp8_product_part_bytes(p.T, p.Nw, p.Kw, p.dx, p.r);
+  if (need > 0 && (!p.part || p.part_bytes < need)) return hipErrorInvalidValue;
+  if (few) {
+    FewLaunch F{};
+    F.w = small_tiles_launch(p, plan);
+    F.w.p.r = 0;
+    F.w.partial = 1;
+    const unsigned tiles = (unsigned)(((int64_t)F.w.mt * F.w.nt * F.w.nsplit + 7) / 8 * 8);
+    FinishLaunch E{p.part, plan.nsplit, p.T, feats, p.G, 1, p.r, p.s, p.M, nullptr, p.C};
+    {
+      KernelEvents ev(KID_FP8_GEMM);
+      if (p.dx) {
+        hipExtLaunchKernelGGL(k_fp8_wide_128_dx, dim3(tiles), dim3(256), 0, stream, ev.start(), ev.stop(), 0, F.w);
+      } else {
+        F.d.X = p.X; F.d.Xs = p.Xs; F.d.A = p.A; F.d.T = p.T; F.d.K = p.Kw; F.d.r = p.r;
+        F.upart = p.part + (size_t)plan.nsplit * p.T * feats;
+        F.jtiles = (p.r + 15) / 16;
+        F.uranges = (int32_t)few_ranges(p.T, p.Kw, p.r);
+        F.chunks = (int32_t)((p.Kw + 127) / 128);
+        F.chunks_per_range = (F.chunks + F.uranges - 1) / F.uranges;
+        F.uwgs = (int32_t)(((p.T + 15) / 16 * F.jtiles * F.uranges + 7) / 8 * 8);
+        E.V = F.upart;
+        E.vranges = F.uranges;
+        E.U = p.U;
+        hipExtLaunchKernelGGL(k_fp8_few, dim3(F.uwgs + tiles), dim3(256), 0, stream, ev.start(), ev.stop(), 0, F);
+      }
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    KernelEvents ev(KID_REDUCE);
+    const dim3 grid((unsigned)((feats + 255) / 256), (unsigned)((p.T + kFewT - 1) / kFewT));
+    hipExtLaunchKernelGGL(p.dx ? k_fp8_finish<true> : k_fp8_finish<false>, grid, dim3(256), 0, stream, ev.start(),
+                          ev.stop(), 0, E);
+    return hipGetLastError();
+  }
   hipError_t e = launch_tiles<4>(p, 0, plan.wide, plan, stream);
   if (e == hipSuccess) e = launch_tiles<2>(p, plan.wide, feats, plan, stream);
   if (e != hipSuccess || plan.nsplit == 1) return e;

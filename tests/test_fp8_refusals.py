@@ -128,15 +128,12 @@ def test_checkpoint_backward_pointers():
 
 
 def test_workspaces_hold_what_they_are_said_to():
-    """r = 0 needs no adapter scratch; the sizes grow with T and r and never overflow a call's own limits."""
+    """No tokens, or no adapter where only it needs scratch: none.  Else at least the 8-bit form of dY, U and G."""
     assert q.qlora_fp8_fwd_workspace_bytes(256, 256, 0, 8) == 0
     assert q.qlora_checkpoint_workspace_bytes(256, 256, 8, 0) == 0
-    for T in (1, 16, 17, 100, 1000, 4096):
-        prev = -1
-        for r in (0, 8, 64, 128):
-            n = q.qlora_fp8_bwd_workspace_bytes(1024, 2048, T, r)
-            assert n >= T * 1024 + T * 8 + T * r * 8 and n > prev
-            prev = n
+    for T in (1, 16, 17, 100, 128, 129, 1000, 4096):
+        for r in (0, 1, 8, 64, 128):
+            assert q.qlora_fp8_bwd_workspace_bytes(1024, 2048, T, r) >= T * 1024 + T * 8 + T * r * 8
 
 
 # ---------------------------------------------------------------------------

@@ -74,14 +74,6 @@ __global__ __launch_bounds__(NW * 64) void k_fp8_down(DownLaunch L) {
     for (int w = 1; w < NW; ++w) v += red[w][rr][j];
     return v;
   };
-  if (L.nsplit > 1) {
-    float* part = p.part + (int64_t)split * p.T * p.r;
-    for (int e = threadIdx.x; e < TOK * COL; e += NW * 64) {
-      const int rr = e / COL, j = e % COL;
-      if (t0 + rr < p.T && j0 + j < p.r) part[(t0 + rr) * p.r + j0 + j] = sum(rr, j);
-    }
-    return;
-  }
   // this workgroup's columns of U, their hi and lo columns of Us, and (its
   // share of) the padding
   for (int e = threadIdx.x; e < TOK * COL; e += NW * 64) {
@@ -115,16 +107,123 @@ __global__ __launch_bounds__(256) void k_fp8_down_sum(DownLaunch L) {
   });
 }
 
-// many tokens: 64 x r tiles, the contraction split until the workgroups fill
-// the CUs; fewer: 16 x 16 tiles over the whole contraction, in one launch
+// ---------------------------------------------------------------------------
+// down for many tokens
+//
+// A workgroup of eight waves owns 128 tokens and all of U's columns (16 JT) for
+// one range of the contraction, a chunk of 128 positions at a time: X's codes
+// [128][128 B] and A's rows [16 JT][256 B] are copied straight into one of PD
+// LDS stages, PD - 1 chunks ahead; wave w multiplies tokens 16 w .. +15.  The
+// range's scales (at most 32 chunks) are in LDS from the start, so nothing but
+// the copies is in flight in the loop.  Fragments loaded from global memory (the
+// tiles above) cost 64 cache lookups a load: 18 us at 4096 x 8192, r = 64,
+// against 13 here (33.5 MB of codes).
+// ---------------------------------------------------------------------------
+constexpr int kManyTok = 128;
+constexpr int kManyRange = 32;  // chunks of a range at most
+
+template <int JT>
+__global__ __launch_bounds__(512) void k_fp8_down_many(DownLaunch L) {
+  constexpr int PD = JT <= 4 ? 4 : 3;
+  constexpr int kX = kManyTok * 128, kA = 16 * JT * 256, kStage = kX + kA;
+  constexpr int NA = JT <= 2 ? 1 : JT / 2;  // copies of A a wave and chunk
+  constexpr int NC = 2 + NA;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PD * kStage + 1024];
+  __shared__ uint32_t sc[kManyTok][kManyRange / 4];
+  const Fp8DownParams& p = L.p;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = lane & 15, g = lane >> 4;
+  const int split = (int)blockIdx.x / L.ttiles;
+  const int64_t t0 = (int64_t)((int)blockIdx.x - split * L.ttiles) * kManyTok;
+  const int c_begin = split * L.chunks_per_split;  // a multiple of four
+  const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
+  const int64_t ldx = fp8_scale_ld(p.K);
+
+  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) {
+    const int t = e / (kManyRange / 4), d = e % (kManyRange / 4);
+    uint32_t v = 0x7F7F7F7Fu;
+    if (t0 + t < p.T && c_begin + 4 * d < c_end) v = reinterpret_cast<const uint32_t*>(p.Xs + (t0 + t) * ldx + c_begin)[d];
+    sc[t][d] = v;
+  }
+  dma::wait_vm<0>();
+
+  const dma::v4i_t rx = dma::rsrc(p.X + t0 * p.K, (p.T - t0) * p.K), ra = dma::rsrc(p.A, (int64_t)p.r * p.K * 2);
+  const uint32_t lds0 = LDS_ADDR(lds);
+  auto issue = [&](int c) {
+    const int ch = c_begin + c;
+    const bool in = ch < c_end;
+    const uint32_t st = lds0 + (uint32_t)(c % PD * kStage);
+    const int64_t k0 = (int64_t)ch * 128;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // rows 16 w + 8 j .. +7: piece of row R at piece ^ R % 8 ^ R / 8 % 2
+      const int R = 16 * wave + 8 * j + (lane >> 3);
+      const int64_t k = k0 + 16 * ((lane & 7) ^ (lane >> 3) ^ j);
+      dma::copy16(rx, in && t0 + R < p.T && k < p.K ? (uint32_t)(R * p.K + k) : dma::kOob, st + 2048 * wave + 1024 * j);
+    }
+#pragma unroll
+    for (int j = 0; j < NA; ++j) {  // four rows of A: piece of row R at piece ^ R % 16
+      const int blk = NA * wave + j;
+      const int R = 4 * blk + (lane >> 4);
+      const int64_t k = k0 + 8 * (i ^ (R & 15));
+      // with 16 columns the last waves have nothing to copy: so that every wave
+      // counts alike, theirs read nothing and fill the kilobyte behind the stages
+      const bool mine = blk < 4 * JT;
+      dma::copy16(ra, in && mine && R < p.r && k < p.K ? (uint32_t)((R * p.K + k) * 2) : dma::kOob,
+                  mine ? st + kX + 1024 * blk : lds0 + PD * kStage);
+    }
+  };
+
+  f32x4_t acc[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int n = c_end - c_begin;
+#pragma unroll
+  for (int c = 0; c < PD - 1; ++c) issue(c);
+  for (int c = 0; c < n; ++c) {
+    dma::wait_vm<(PD - 2) * NC>();  // this wave's copies of chunk c have landed
+    lds_barrier();                  // everybody's have, and chunk c - 1 is read
+    issue(c + PD - 1);
+    const uint8_t* X = lds + c % PD * kStage;
+    const uint8_t* A = X + kX;
+    const int R = 16 * wave + i, sw = (i & 7) ^ (i >> 3);
+    const u32x4_t x0 = *reinterpret_cast<const u32x4_t*>(X + R * 128 + (((2 * g) ^ sw) << 4));
+    const u32x4_t x1 = *reinterpret_cast<const u32x4_t*>(X + R * 128 + (((2 * g + 1) ^ sw) << 4));
+    const float k = scale_of(sc[R][c >> 2] >> (8 * (c & 3)) & 0xFFu);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const u32x4_t x = q < 2 ? x0 : x1;
+      const bf16x8_t xa = __builtin_bit_cast(bf16x8_t, restore8(x[2 * (q & 1)], x[2 * (q & 1) + 1], k));
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt)
+        acc[jt] = mfma16(xa, *reinterpret_cast<const bf16x8_t*>(A + (16 * jt + i) * 256 + (((4 * g + q) ^ i) << 4)), acc[jt]);
+    }
+  }
+  dma::wait_vm<0>();  // no copy may land in LDS that is no longer this workgroup's
+
+  // lane l, value v: token 16 w + 4 (l/16) + v, column 16 jt + l % 16
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t t = t0 + 16 * wave + 4 * g + v;
+    if (t >= p.T) continue;
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const int j = 16 * jt + i;
+      if (j < p.r) p.part[((int64_t)split * p.T + t) * p.r + j] = acc[jt][v];
+    }
+  }
+}
+
+// Many tokens: 128 x r tiles, the contraction in as many ranges of at most 32
+// chunks (whole dwords of scales) as fill the CUs; their sums are added by
+// k_fp8_down_sum.  Fewer: 16 x 16 tiles over the whole contraction, one launch.
 constexpr int64_t kDownManyT = 512;
-int down_rt(int r) { return r <= 64 ? 4 : 2; }
-int down_splits(int64_t T, int64_t K, int r) {
-  if (T < kDownManyT) return 1;
-  const int64_t tiles = (T + 16 * down_rt(r) - 1) / (16 * down_rt(r)), chunks = (K + 127) / 128;
+int down_ranges(int64_t T, int64_t K, int32_t& per) {
+  const int64_t tiles = (T + kManyTok - 1) / kManyTok, chunks = (K + 127) / 128;
   int64_t s = 256 / tiles;
-  if (s > chunks / 8) s = chunks / 8;
-  return (int)(s < 1 ? 1 : s);
+  if (s < (chunks + kManyRange - 1) / kManyRange) s = (chunks + kManyRange - 1) / kManyRange;
+  per = (int32_t)(((chunks + s - 1) / s + 3) / 4 * 4);
+  return (int)((chunks + per - 1) / per);
 }
 
 // ---------------------------------------------------------------------------
@@ -322,38 +421,38 @@ int grad_splits(int64_t T, int64_t K, int64_t N) {
 }  // namespace
 
 size_t fp8_down_part_bytes(int64_t T, int64_t K, int r) {
-  const int s = down_splits(T, K, r);
-  return s > 1 ? (size_t)s * T * r * 4 : 0;
+  int32_t per;
+  return T < kDownManyT ? 0 : (size_t)down_ranges(T, K, per) * T * r * 4;
 }
 
 hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream) {
   DownLaunch L{};
   L.p = p;
   L.chunks = (int32_t)((p.K + 127) / 128);
-  L.nsplit = down_splits(p.T, p.K, p.r);
-  L.chunks_per_split = (L.chunks + L.nsplit - 1) / L.nsplit;
-  if (L.nsplit > 1 && (!p.part || p.part_bytes < fp8_down_part_bytes(p.T, p.K, p.r))) return hipErrorInvalidValue;
   const int jt = (p.r + 15) / 16;
+  const bool many = p.T >= kDownManyT;
+  if (many && (!p.part || p.part_bytes < fp8_down_part_bytes(p.T, p.K, p.r))) return hipErrorInvalidValue;
   {
     KernelEvents ev(KID_FP8_DOWN);
     const hipEvent_t e0 = ev.start(), e1 = ev.stop();
-    if (p.T < kDownManyT) {
+    if (!many) {
+      L.nsplit = 1;
+      L.chunks_per_split = L.chunks;
       L.ttiles = (int32_t)((p.T + 15) / 16);
       L.jtiles = jt;
       hipExtLaunchKernelGGL((k_fp8_down<1, 1, 16>), dim3((unsigned)(L.ttiles * L.jtiles)), dim3(1024), 0, stream, e0, e1, 0, L);
     } else {
-      const int tok = 16 * down_rt(p.r);
-      L.ttiles = (int32_t)((p.T + tok - 1) / tok);
-      L.jtiles = 1;
+      L.nsplit = down_ranges(p.T, p.K, L.chunks_per_split);
+      L.ttiles = (int32_t)((p.T + kManyTok - 1) / kManyTok);
       const dim3 grid((unsigned)(L.ttiles * L.nsplit)), block(512);
-      if (jt == 1) hipExtLaunchKernelGGL((k_fp8_down<4, 1, 8>), grid, block, 0, stream, e0, e1, 0, L);
-      else if (jt == 2) hipExtLaunchKernelGGL((k_fp8_down<4, 2, 8>), grid, block, 0, stream, e0, e1, 0, L);
-      else if (jt <= 4) hipExtLaunchKernelGGL((k_fp8_down<4, 4, 8>), grid, block, 0, stream, e0, e1, 0, L);
-      else hipExtLaunchKernelGGL((k_fp8_down<2, 8, 8>), grid, block, 0, stream, e0, e1, 0, L);
+      if (jt == 1) hipExtLaunchKernelGGL(k_fp8_down_many<1>, grid, block, 0, stream, e0, e1, 0, L);
+      else if (jt == 2) hipExtLaunchKernelGGL(k_fp8_down_many<2>, grid, block, 0, stream, e0, e1, 0, L);
+      else if (jt <= 4) hipExtLaunchKernelGGL(k_fp8_down_many<4>, grid, block, 0, stream, e0, e1, 0, L);
+      else hipExtLaunchKernelGGL(k_fp8_down_many<8>, grid, block, 0, stream, e0, e1, 0, L);
     }
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || L.nsplit == 1) return e;
+  if (e != hipSuccess || !many) return e;
   KernelEvents ev(KID_REDUCE);
   hipExtLaunchKernelGGL(k_fp8_down_sum, dim3((unsigned)((p.T * p.ldh + 255) / 256)), dim3(256), 0, stream, ev.start(),
                         ev.stop(), 0, L);

@@ -150,6 +150,12 @@ LAYERS = [
     (448, 4096, 2100, 24),  # 256 x 256 tiles backward
     (1024, 4160, 2304, 64),
     (64, 4096, 2304, 8),    # a contraction of 64
+    (320, 640, 700, 128),   # the largest rank, many tokens
+    (256, 4480, 640, 40),   # 35 blocks of contraction, a rank of 8 mod 16
+    (128, 5184, 128, 5),    # the most tokens of the one-launch form, odd rank, 40.5 blocks
+    (5184, 128, 128, 128),  # and backward
+    (128, 256, 129, 16),    # one token more
+    (8192, 512, 3, 1),      # rank 1
 ]
 
 
@@ -207,6 +213,34 @@ def test_layer(N, K, T, r):
     # again: the same bits
     Y2, _ = q.qlora_fp8_linear_fwd(*forms, A, B, alpha)
     assert torch.equal(Y, Y2)
+
+
+def test_without_u_and_with_one_row_of_u():
+    """want_u=False gives the same Y; a U_out of the caller's is what is returned."""
+    import torch
+    q = _q()
+    for T in (3, 200, 600):
+        inp = _layer(256, 320, T, 8, seed=T)
+        forms, _, _ = _forms(inp)
+        A, B = dev_bf16(inp["A"]), dev_bf16(inp["B"])
+        Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0)
+        Y2, none = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0, want_u=False)
+        mine = torch.full_like(U, 7.0)
+        Y3, U3 = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0, U_out=mine)
+        assert none is None and U3 is mine and torch.equal(Y2, Y) and torch.equal(Y3, Y) and torch.equal(mine, U)
+
+
+def test_rows_of_a_batch_are_those_of_the_whole():
+    """Sums do not depend on the other tokens: a contraction of one range gives a token the same bits in any batch
+    of the same cut."""
+    import torch
+    q = _q()
+    inp = _layer(256, 448, 300, 8, seed=5)
+    forms, _, _ = _forms(inp)
+    A, B = dev_bf16(inp["A"]), dev_bf16(inp["B"])
+    Y, U = q.qlora_fp8_linear_fwd(*forms, A, B, 16.0)
+    Y2, U2 = q.qlora_fp8_linear_fwd(forms[0], forms[1], forms[2][20:290], forms[3][20:290], A, B, 16.0)
+    assert torch.equal(Y[20:290], Y2) and torch.equal(U[20:290], U2)
 
 
 def test_no_tokens():

@@ -638,9 +638,22 @@ ProductPlan plan_product(int64_t T, int64_t feats, int64_t len, bool few) {
   const int64_t mt4 = (T + 255) / 256, nt4 = (feats + 255) / 256, mt2 = (T + 127) / 128;
   const auto small_tiles = [&](int64_t f) { return mt2 * ((f + 127) / 128); };
   ProductPlan best{0, 1, (uint32_t)(groups * 8)};
+  if (few) {
+    // a stream of the weight: ranges of 2048 (256 KB of it a workgroup), more
+    // where those give fewer workgroups than CUs.  One token through 28672 x
+    // 8192: 54 us at 4 ranges, 64 at 2, 61 at 8; 100 through 22016 x 8192: 74 at
+    // 4, 81 at 2 and at 8
+    int64_t s = (groups + 3) / 4;
+    const int64_t fill = (256 + small_tiles(feats) - 1) / small_tiles(feats);
+    if (s < fill) s = fill;
+    if (s > groups) s = groups;
+    if (s > 16) s = 16;
+    const int64_t per = (groups + s - 1) / s;
+    return ProductPlan{0, (int32_t)((groups + per - 1) / per), (uint32_t)(per * 8)};
+  }
   double time = small_time(small_tiles(feats), steps);
   // whole rounds of large tiles, the last features on small ones; or large tiles alone
-  for (int64_t rounds = 1; !few; ++rounds) {
+  for (int64_t rounds = 1;; ++rounds) {
     const int64_t cols = rounds * 256 / mt4 < nt4 ? rounds * 256 / mt4 : nt4;
     if (cols > 0) {
       const int64_t wide = cols * 256 < feats ? cols * 256 : feats;

@@ -85,16 +85,13 @@ __device__ __forceinline__ f32x16_t mfma8(v8i_t a, v8i_t b, f32x16_t c, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, Q, (int)sa, Q, (int)sb);
 }
 
-// A copy into LDS that the compiler does not count (see dma.hpp): behind one
-// that it knows of, it would wait for every copy in flight before a
-// transposing read.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void copy16_uncounted(dma::v4i_t r, uint32_t voff, uint32_t soff, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(voff), "s"(r), "s"(soff)
-               : "memory", "m0");
+// Eight rows of a lane's column, read transposed.  The pointer is restrict-
+// qualified: the slot read is never one that a copy in flight writes (the waits
+// and the barrier of each pair see to it), and without the word the compiler
+// drains every copy before such a read.
+__device__ __forceinline__ v2i_t read_tr8(const uint8_t* __restrict__ slot, uint32_t off) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i_t*)((lds_u8_t*)slot + off));
 }
-#pragma clang diagnostic pop
 
 // DX: the weight's contraction runs down its rows; S: 32 x 32 tiles of a wave
 // each way (4: tiles of 256 x 256, a workgroup per CU; 2: 128 x 128, two).
@@ -145,8 +142,6 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
   const int64_t xbase = t0 * len + k0, wbase = DX ? k0 * p.Kw + f0 : f0 * len + k0;
   const int64_t xbytes = (p.T - t0) * len - k0, wbytes = p.Nw * p.Kw - wbase;
   const __amdgpu_buffer_rsrc_t rx = buf(p.X + xbase, xbytes), rw = buf(p.W + wbase, wbytes);
-  const dma::v4i_t ax = dma::rsrc(p.X + xbase, xbytes), aw = dma::rsrc(p.W + wbase, wbytes);  // dx
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8_t*)lds);
   const __amdgpu_buffer_rsrc_t rs = buf(p.Xs, p.T * fp8_scale_ld(len));
 
   // copies of a pair of steps: eight kilobytes of each operand a wave.  Rows
@@ -170,13 +165,11 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
   // copy j (0 .. NC - 1) of X's or W's pair `pr` into a slot
   auto copy_x = [&](uint32_t pr, uint32_t slot, int j) {
     const uint32_t at = pr < pairs ? pr : pairs - 1;
-    if (DX) copy16_uncounted(ax, xoff[j], at * 128u, lds0 + slot + kSlot / 4 * wave + 1024 * j);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, xoff[j], at * 128u, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, xoff[j], at * 128u, 0, 0);
   };
   auto copy_w = [&](uint32_t pr, uint32_t slot, int j) {
     const uint32_t at = pr < pairs ? pr : pairs - 1;
-    if (DX) copy16_uncounted(aw, woff[j], at * wpair, lds0 + slot + kSlot / 4 * wave + 1024 * j);
-    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, woff[j], at * wpair, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(lds + slot + kSlot / 4 * wave + 1024 * j), 16, woff[j], at * wpair, 0, 0);
   };
 
   // scales: a dword holds the bytes of four blocks, eight steps
@@ -187,13 +180,9 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
     const int64_t row = t0 + wt + 32 * t + c32;
     soff[t] = (uint32_t)((row < p.T ? row : p.T - 1) * fp8_scale_ld(len) + k0 / 128);
   }
-  // X's: a dword a group; for dx, whose copies are uncounted and drained by
-  // the wait for a counted load, four dwords in every fourth group (3% faster
-  // there, and as much slower where the copies are counted)
   auto load_sx = [&](uint32_t gr, int t) {
     return __builtin_amdgcn_raw_buffer_load_b32(rs, soff[t], (gr < groups ? gr : groups - 1) * 4u, 0);
   };
-  auto load_sx4 = [&](uint32_t quad, int t) { return __builtin_amdgcn_raw_buffer_load_b128(rs, soff[t], quad * 16u, 0); };
   // the wave's features lie in one block of the weight: its bytes lie in one
   // row of the weight's scales, or, for dx, in one column of them
   const int64_t fb = __builtin_amdgcn_readfirstlane((uint32_t)((f0 + wf < feats ? f0 + wf : f0) / 128));
@@ -241,7 +230,7 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
     if (DX) {
 #pragma unroll
       for (int q = 2 * e; q < 2 * e + 2; ++q) {
-        const v2i_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i_t*)((lds_u8_t*)lds + slot + wpos[f] + WF * (64 * h + 8 * q)));
+        const v2i_t v = read_tr8(lds + slot, wpos[f] + WF * (64 * h + 8 * q));
         F.w[f][e][2 * (q & 1)] = (uint32_t)v[0];
         F.w[f][e][2 * (q & 1) + 1] = (uint32_t)v[1];
       }
@@ -265,18 +254,10 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
       for (int v = 0; v < 16; ++v) acc[f][t][v] = 0.0f;
 
   uint32_t sx[S], sxn[S], swc;
-  u32x4_t sxq[S];
   SwRaw swn;
   Frags F[2];
 #pragma unroll
-  for (int t = 0; t < S; ++t) {
-    if (DX) {
-      sxq[t] = load_sx4(0, t);
-      sx[t] = sxq[t][0];
-    } else {
-      sx[t] = sxn[t] = load_sx(0, t);
-    }
-  }
+  for (int t = 0; t < S; ++t) sx[t] = sxn[t] = load_sx(0, t);
   swn = load_sw(0);
   swc = sw_of(swn);
   __builtin_amdgcn_sched_barrier(0);
@@ -299,7 +280,7 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
   // to be counted (behind the loop nothing uses them, and they are gone)
   auto step = [&](uint32_t u, auto j_, auto in_loop_) {
     constexpr int J = decltype(j_)::value, Q = J / 2;
-    constexpr bool loads = decltype(in_loop_)::value && !DX;
+    constexpr bool loads = decltype(in_loop_)::value;
     constexpr bool odd = J % 2 != 0;
     Frags& C = F[odd];
     Frags& Nx = F[!odd];
@@ -351,29 +332,10 @@ __device__ __forceinline__ void product(const WideLaunch& L, const uint32_t bid,
     swc = sw_of(swn);
   };
   uint32_t u = 0;
-  if (DX) {
-    for (uint32_t quad = 1; u + 8 <= nsteps; ++quad) {
-      u32x4_t nq[S];
+  for (; u + 8 <= nsteps; u += 8) {
+    steps8(u);
 #pragma unroll
-      for (int t = 0; t < S; ++t) nq[t] = load_sx4(quad, t);  // past the row's end: not used
-      for (int k = 1; k <= 4 && u + 8 <= nsteps; ++k, u += 8) {
-        steps8(u);
-#pragma unroll
-        for (int t = 0; t < S; ++t) sx[t] = k == 1 ? sxq[t][1] : k == 2 ? sxq[t][2] : sxq[t][3];
-      }
-#pragma unroll
-      for (int t = 0; t < S; ++t) sxq[t] = nq[t];
-      if (u % 32 == 0) {
-#pragma unroll
-        for (int t = 0; t < S; ++t) sx[t] = sxq[t][0];
-      }
-    }
-  } else {
-    for (; u + 8 <= nsteps; u += 8) {
-      steps8(u);
-#pragma unroll
-      for (int t = 0; t < S; ++t) sx[t] = sxn[t];
-    }
+    for (int t = 0; t < S; ++t) sx[t] = sxn[t];
   }
   if (u < nsteps) step(u, std::integral_constant<int, 0>(), std::false_type());
   if (u + 1 < nsteps) step(u + 1, std::integral_constant<int, 1>(), std::false_type());

@@ -9,6 +9,7 @@
 #include "dma.hpp"
 #include "fp8.hpp"
 #include "fp8_down.hpp"
+#include "fp8_sum.hpp"
 #include "lds_tr.hpp"
 #include "trace.hpp"
 
@@ -101,9 +102,7 @@ __global__ __launch_bounds__(256) void k_fp8_down_sum(DownLaunch L) {
   if (e >= p.T * p.ldh) return;
   const int64_t t = e / p.ldh;
   down_out(p, t, (int)(e - t * p.ldh), [&](int j) {
-    float v = p.part[t * p.r + j];
-    for (int q = 1; q < L.nsplit; ++q) v += p.part[((int64_t)q * p.T + t) * p.r + j];
-    return v;
+    return ordered_sum(L.nsplit, [&](int q) { return p.part[((int64_t)q * p.T + t) * p.r + j]; });
   });
 }
 
@@ -394,12 +393,7 @@ __global__ __launch_bounds__(256) void k_fp8_grad_sum(GradLaunch L) {
   const int64_t na = (int64_t)p.r * p.K, n = na + (int64_t)p.r * p.N;
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= n) return;
-  f32x4_t v = *reinterpret_cast<const f32x4_t*>(p.part + e);
-  for (int q = 1; q < L.nsplit; ++q) {
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(p.part + q * n + e);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] += w[x];
-  }
+  f32x4_t v = ordered_sum(L.nsplit, [&](int q) { return *reinterpret_cast<const f32x4_t*>(p.part + q * n + e); });
   f32x4_t* dst = reinterpret_cast<f32x4_t*>(e < na ? p.dA + e : p.dB + (e - na));
   if (p.accumulate) {
     const f32x4_t o = *dst;

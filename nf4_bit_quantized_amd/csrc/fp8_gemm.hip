@@ -48,6 +48,7 @@
 #include "dma.hpp"
 #include "fp8.hpp"
 #include "fp8_down.hpp"
+#include "fp8_sum.hpp"
 #include "fp8_tail.hpp"
 #include "trace.hpp"
 
@@ -439,8 +440,9 @@ __global__ __launch_bounds__(256, 2) void k_fp8_wide_128_dx(WideLaunch L) {
 // Few tokens.  The product is a stream of the weight, and what costs beside it
 // is launches: U = X A^T runs in the same one, its workgroups first, and the
 // pass that adds the contraction ranges' partial sums also forms the rank-r
-// term from U (or, for dx, from G), in fp32.  One token through 28672 x 8192
-// at r = 64: 49 us against 56 with U and the sums in launches of their own.
+// term from U (or, for dx, from G), in fp32.  One token through 28672 x 8192 at
+// r = 64, the weight read from HBM: 50 us (4.8 TB/s), of which the last pass 6;
+// with U and the sums in launches of their own 8 more.
 struct FewLaunch {
   WideLaunch w;
   Fp8DownParams d;
@@ -474,7 +476,7 @@ __global__ __launch_bounds__(256, 2) void k_fp8_few(FewLaunch L) {
 // C[t][f] = bf16( sum over the ranges of part[q][t][f] + s sum_j V[t][j] M ),
 // V being U (its ranges' partial sums added here, and U written) or G, M B[f][j]
 // or, for dx, A[j][f].  A workgroup: kFewT tokens, a feature a thread.
-constexpr int kFewT = 8;
+constexpr int kFewT = 8, kFewF = 128, kFewQ = 4;
 constexpr int kFewMaxRank = 128;
 
 struct FinishLaunch {
@@ -491,63 +493,96 @@ struct FinishLaunch {
 };
 
 template <bool DX>
-__global__ __launch_bounds__(256) void k_fp8_finish(FinishLaunch L) {
+__global__ __launch_bounds__(kFewF) void k_fp8_finish(FinishLaunch L) {
   __shared__ float v[kFewT][kFewMaxRank];
   const int64_t t0 = (int64_t)blockIdx.y * kFewT;
   const int nt = (int)(L.T - t0 < kFewT ? L.T - t0 : kFewT);
   const int r = L.r;
-  for (int e = threadIdx.x; e < kFewT * r; e += 256) {
+  const int64_t f = (int64_t)blockIdx.x * kFewF + threadIdx.x;
+  const int64_t fc = f < L.feats ? f : L.feats - 1;
+  // tokens past the last repeat it, and are not stored
+  int64_t row[kFewT];
+  float part[kFewQ][kFewT];
+  const auto load_part = [&](int q0) {
+#pragma unroll
+    for (int q = 0; q < kFewQ; ++q) {
+      const float* src = L.part + (int64_t)(q0 + q < L.nsplit ? q0 + q : L.nsplit - 1) * L.T * L.feats;
+#pragma unroll
+      for (int t = 0; t < kFewT; ++t) part[q][t] = src[row[t]];
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < kFewT; ++t) row[t] = (t0 + (t < nt ? t : nt - 1)) * L.feats + fc;
+  load_part(0);
+  // M's first columns, 64 of them where its rows can be read 16 bytes at a time
+  const bool wide = !DX && r % 8 == 0;
+  const int64_t sj = DX ? L.feats : 1;
+  const uint16_t* m0 = DX ? L.M + fc : L.M + fc * r;
+  u32x4_t mw[8];
+  uint16_t mn[16];
+  const auto load_m = [&](int j0) {
+    if (wide) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) mw[q] = *reinterpret_cast<const u32x4_t*>(m0 + (j0 + 8 * q < r ? j0 + 8 * q : r - 8));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) mn[q] = m0[(j0 + q < r ? j0 + q : r - 1) * sj];
+    }
+  };
+  load_m(0);
+  for (int e = threadIdx.x; e < kFewT * r; e += kFewF) {
     const int t = e / r, j = e - t * r;
     if (t >= nt) {
       v[t][j] = 0.0f;
       continue;
     }
-    float u = L.V[(t0 + t) * r + j];
-    for (int q = 1; q < L.vranges; ++q) u += L.V[((int64_t)q * L.T + t0 + t) * r + j];
+    const float* src = L.V + (t0 + t) * r + j;
+    const float u = ordered_sum(L.vranges, [&](int q) { return src[(int64_t)q * L.T * r]; });
     v[t][j] = L.s * u;
     if (L.U && blockIdx.x == 0) L.U[(t0 + t) * r + j] = u;
   }
   __syncthreads();
-  const int64_t f = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (f >= L.feats) return;
-  // tokens past the last repeat it, and are not stored
-  int64_t row[kFewT];
   float acc[kFewT];
 #pragma unroll
-  for (int t = 0; t < kFewT; ++t) {
-    row[t] = (t0 + (t < nt ? t : nt - 1)) * L.feats + f;
-    acc[t] = L.part[row[t]];
-  }
-  for (int q = 1; q < L.nsplit; ++q) {
-    const float* src = L.part + (int64_t)q * L.T * L.feats;
+  for (int t = 0; t < kFewT; ++t) acc[t] = part[0][t];
+  for (int q0 = 0;;) {
 #pragma unroll
-    for (int t = 0; t < kFewT; ++t) acc[t] += src[row[t]];
+    for (int q = 0; q < kFewQ; ++q)
+      if (q0 + q > 0 && q0 + q < L.nsplit) {
+#pragma unroll
+        for (int t = 0; t < kFewT; ++t) acc[t] += part[q][t];
+      }
+    q0 += kFewQ;
+    if (q0 >= L.nsplit) break;
+    load_part(q0);
   }
-  auto add = [&](int j, float m) {
+  const auto add = [&](int j, float m) {
 #pragma unroll
     for (int t = 0; t < kFewT; ++t) acc[t] = fmaf(v[t][j], m, acc[t]);
   };
-  if (DX) {
-    int j = 0;
-    for (; j + 8 <= r; j += 8) {
-      uint16_t m[8];
+  for (int j0 = 0;;) {
+    if (wide) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m[q] = L.M[(int64_t)(j + q) * L.feats + f];
+      for (int q = 0; q < 8; ++q) {
+        if (j0 + 8 * q < r) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) add(j + q, bf16_bits_to_f32(m[q]));
-    }
-    for (; j < r; ++j) add(j, bf16_bits_to_f32(L.M[(int64_t)j * L.feats + f]));
-  } else if (r % 8 == 0) {
-    for (int j = 0; j < r; j += 8) {
-      const u32x4_t m = *reinterpret_cast<const u32x4_t*>(L.M + f * r + j);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        add(j + 2 * q, bf16_bits_to_f32(m[q] & 0xFFFFu));
-        add(j + 2 * q + 1, bf16_bits_to_f32(m[q] >> 16));
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t m = mw[q][h];
+            add(j0 + 8 * q + 2 * h, bf16_bits_to_f32(m & 0xFFFFu));
+            add(j0 + 8 * q + 2 * h + 1, bf16_bits_to_f32(m >> 16));
+          }
+        }
       }
+      j0 += 64;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (j0 + q < r) add(j0 + q, bf16_bits_to_f32(mn[q]));
+      j0 += 16;
     }
-  } else {
-    for (int j = 0; j < r; ++j) add(j, bf16_bits_to_f32(L.M[f * r + j]));
+    if (j0 >= r) break;
+    load_m(j0);
   }
 #pragma unroll
   for (int t = 0; t < kFewT; ++t)
@@ -563,8 +598,7 @@ __global__ __launch_bounds__(256) void k_fp8_sum(const float* __restrict__ part,
                                                  uint16_t* __restrict__ C) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= n) return;
-  f32x4_t v = *reinterpret_cast<const f32x4_t*>(part + e);
-  for (int q = 1; q < nsplit; ++q) v += *reinterpret_cast<const f32x4_t*>(part + q * n + e);
+  const f32x4_t v = ordered_sum(nsplit, [&](int q) { return *reinterpret_cast<const f32x4_t*>(part + q * n + e); });
   *reinterpret_cast<uint2*>(C + e) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
@@ -728,8 +762,8 @@ hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     KernelEvents ev(KID_REDUCE);
-    const dim3 grid((unsigned)((feats + 255) / 256), (unsigned)((p.T + kFewT - 1) / kFewT));
-    hipExtLaunchKernelGGL(p.dx ? k_fp8_finish<true> : k_fp8_finish<false>, grid, dim3(256), 0, stream, ev.start(),
+    const dim3 grid((unsigned)((feats + kFewF - 1) / kFewF), (unsigned)((p.T + kFewT - 1) / kFewT));
+    hipExtLaunchKernelGGL(p.dx ? k_fp8_finish<true> : k_fp8_finish<false>, grid, dim3(kFewF), 0, stream, ev.start(),
                           ev.stop(), 0, E);
     return hipGetLastError();
   }

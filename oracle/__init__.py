@@ -14,6 +14,7 @@ describe, step by step and in the pages' order:
   4-bit indices, nibble packing, double quantization of the scales, dequant.
 * ``oracle.lora`` -- the two-branch forward, the frozen-base backward, merge.
 * ``oracle.bf16`` -- the oracle's own bfloat16 round-to-nearest-even.
+* ``oracle.fp8``  -- the 8-bit form and the layer over 8-bit operands.
 * ``oracle.optim`` -- the AdamW update of the adapter parameters.
 
 Page keys used in citations (titles of the pages the method is read from):

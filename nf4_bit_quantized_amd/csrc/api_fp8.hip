@@ -84,6 +84,7 @@ Fp8BwdWs plan_bwd(int64_t N, int64_t K, int64_t T, int32_t r, void* ws) {
       if (T > kFp8FewT) w.Ap = static_cast<uint16_t*>(c.take((size_t)K * hilo_ld(r) * 2));
       w.part_bytes = std::max(std::max(w.part_bytes, fp8_down_part_bytes(T, K, r)),
                               std::max(lora_g_part_bytes(T, N, r), fp8_grad_part_bytes(T, K, N, r)));
+      if (fp8_form_ok(T, r)) w.part_bytes = std::max(w.part_bytes, fp8_form_part_bytes(T, N, r));
     }
     w.part = static_cast<float*>(c.take(w.part_bytes));
   }
@@ -206,6 +207,7 @@ int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
   }
   const float s = r > 0 ? alpha / (float)r : 0.0f;
   const int64_t ldh = hilo_ld(r);
+  const bool form = fp8_form_ok(T, r);  // G and, for dX, the 8-bit form of dY from one pass over it
   const float* U = U_in;
   if (r > 0) {
     if (!U) {
@@ -213,11 +215,16 @@ int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
       HIP_TRY(launch_fp8_down(Dn, s_));
       U = w.U;
     }
-    const int e = lora_g(dY, B, T, N, r, s, w.part, w.part_bytes, w.G, w.Gs, s_);
-    if (e) return e;
+    if (form) {
+      const Fp8FormParams F{dY, B, T, N, r, s, dX ? w.dYc : nullptr, w.dYs, w.G, w.Gs, ldh, w.part, w.part_bytes};
+      HIP_TRY(launch_fp8_form(F, s_));
+    } else {
+      const int e = lora_g(dY, B, T, N, r, s, w.part, w.part_bytes, w.G, w.Gs, s_);
+      if (e) return e;
+    }
   }
   if (dX) {
-    HIP_TRY(launch_fp8_quantize(dY, QLORA_W_BF16, T, N, 1, w.dYc, w.dYs, s_));
+    if (!form) HIP_TRY(launch_fp8_quantize(dY, QLORA_W_BF16, T, N, 1, w.dYc, w.dYs, s_));
     Fp8Params P{};
     P.X = w.dYc; P.Xs = w.dYs; P.W = W_codes; P.Ws = W_scales;
     P.T = T; P.Nw = N; P.Kw = K; P.dx = 1; P.r = r; P.ldh = ldh;

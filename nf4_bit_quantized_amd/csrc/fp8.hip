@@ -20,13 +20,18 @@
 // All three kernels are bound by HBM: every element is read once and written
 // once, with loads and stores of 8 or 16 bytes a lane.
 #include "fp8.hpp"
+#include "fp8_form.hpp"
 #include "trace.hpp"
 
 namespace qlora {
 namespace {
 
+using fp8::absmax8;
+using fp8::codes8;
+using fp8::scale_byte;
+using fp8::u32x2_t;
+
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 // Eight consecutive elements as fp32 (exact).
@@ -63,25 +68,6 @@ struct Load8 {
   }
 };
 
-// Bits of the largest |x|, what is not finite left out.
-__device__ __forceinline__ uint32_t absmax8(const float (&f)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, f[q]) & 0x7FFFFFFFu;
-    m = u > m ? u : m;
-  }
-  if (m >= 0x7F800000u) {
-    m = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, f[q]) & 0x7FFFFFFFu;
-      m = u < 0x7F800000u && u > m ? u : m;
-    }
-  }
-  return m;
-}
-
 // The largest of the 16 lanes of a row (DPP rotations).
 __device__ __forceinline__ uint32_t row_max(uint32_t m) {
   uint32_t o;
@@ -90,25 +76,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m) {
   o = __builtin_amdgcn_update_dpp(0, m, 0x122, 0xF, 0xF, false); m = o > m ? o : m;  // row_ror:2
   o = __builtin_amdgcn_update_dpp(0, m, 0x121, 0xF, 0xF, false); m = o > m ? o : m;  // row_ror:1
   return m;
-}
-
-__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
-  const int e = (int)((m + 0x1FFFFFu) >> 23) - 8;  // at most 247
-  return (uint32_t)(e < 1 ? 1 : e);
-}
-
-// Eight codes; e in 1 .. 247, so the factor 2^(127 - e) is a normal float and
-// the product is exact wherever the code is not zero.
-__device__ __forceinline__ u32x2_t codes8(const float (&f)[8], uint32_t e) {
-  const float k = __builtin_bit_cast(float, (254u - e) << 23);
-  u32x2_t o;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * k, f[4 * h + 1] * k, 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * k, f[4 * h + 3] * k, w, true);
-    o[h] = (uint32_t)w;
-  }
-  return o;
 }
 
 // 1 x 128 blocks.  A wave owns units of 512 columns of one row: 16 lanes to a

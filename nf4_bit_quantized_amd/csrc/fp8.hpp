@@ -73,6 +73,26 @@ struct Fp8DownParams {
 size_t fp8_down_part_bytes(int64_t T, int64_t K, int r);
 hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream);
 
+// G = dY B and the 8-bit form of dY in one pass over it: G [T][r] fp32, the
+// hi/lo pair of s*G into Gs [T][ldh], zero-padded.  Where fp8_form_ok.
+struct Fp8FormParams {
+  const uint16_t* dY;  // bf16 [T][N]
+  const uint16_t* B;   // bf16 [N][r]
+  int64_t T, N;
+  int32_t r;
+  float s;
+  uint8_t* codes;      // null: G alone
+  uint8_t* scales;
+  float* G;
+  uint16_t* Gs;
+  int64_t ldh;
+  float* part;
+  size_t part_bytes;
+};
+bool fp8_form_ok(int64_t T, int r);
+size_t fp8_form_part_bytes(int64_t T, int64_t N, int r);
+hipError_t launch_fp8_form(const Fp8FormParams& p, hipStream_t stream);
+
 // The adapter's gradients: dA[j][k] = s sum_t G[t][j] X[t][k] over the 8-bit
 // form of X, dB[n][j] = s sum_t dY[t][n] U[t][j]; G, U fp32 [T][r].
 struct Fp8GradParams {

@@ -1,5 +1,6 @@
 // The adapter's products over the 8-bit form of the layer's input (fp8.hip):
 //   down:  U[t][j] = sum_k X[t][k] A[j][k]
+//   form:  G[t][j] = sum_n dY[t][n] B[n][j], and the 8-bit form of dY
 //   grad:  dA[j][k] = s sum_t G[t][j] X[t][k],  dB[n][j] = s sum_t dY[t][n] U[t][j]
 // Every e4m3 code times its power-of-two scale is a bf16 value, so X is
 // restored exactly in registers and enters v_mfma_f32_16x16x32_bf16; sums are
@@ -9,6 +10,7 @@
 #include "dma.hpp"
 #include "fp8.hpp"
 #include "fp8_down.hpp"
+#include "fp8_form.hpp"
 #include "fp8_sum.hpp"
 #include "lds_tr.hpp"
 #include "trace.hpp"
@@ -16,9 +18,12 @@
 namespace qlora {
 namespace {
 
+using fp8::absmax_bf16;
+using fp8::codes8_bf16;
 using fp8::down_tile;
 using fp8::mfma16;
 using fp8::restore8;
+using fp8::scale_byte;
 using fp8::scale_of;
 using fp8::u32x4_t;
 using ldstr::tr_frag_swz;
@@ -223,6 +228,136 @@ int down_ranges(int64_t T, int64_t K, int32_t& per) {
   if (s < (chunks + kManyRange - 1) / kManyRange) s = (chunks + kManyRange - 1) / kManyRange;
   per = (int32_t)(((chunks + s - 1) / s + 3) / 4 * 4);
   return (int)((chunks + per - 1) / per);
+}
+
+// ---------------------------------------------------------------------------
+// form: G and the 8-bit form of dY in one pass over it
+//
+// As down for many tokens: a workgroup of eight waves owns 128 tokens for one
+// range of the contraction, a chunk of 128 columns at a time, dY's [128][256 B]
+// and B's [128][32 JT B] copied into LDS two chunks ahead.  A lane holds 32
+// columns of one row, its share of four MFMAs; four lanes have the row's block
+// and find its largest value, and the lane writes its codes.  B's contraction
+// runs down its rows: transposing reads.
+//
+// Bound by HBM's latency: 4096 x 8192, r = 64 (101 MB read and written): 24 us,
+// 4.2 TB/s, against 16 + 16 for G and the form in launches of their own, which
+// read dY twice; a backward at 512 to 4096 tokens takes 1 to 5% less.  Vector
+// work (the largest value and the codes on 16 bits instead of 32) and the order
+// of the chunks (other ranges' tiles starting at other columns) changed nothing.
+// ---------------------------------------------------------------------------
+struct FormLaunch {
+  Fp8FormParams p;
+  int32_t ttiles, chunks, chunks_per_split;
+};
+
+template <int JT>
+__global__ __launch_bounds__(512) void k_fp8_form(FormLaunch L) {
+  constexpr int PD = 3;
+  constexpr int QLD = 16 * JT, PPR = 2 * JT;  // a row of B: elements, 16-byte pieces
+  constexpr int kP = kManyTok * 256, kB = 128 * QLD * 2, kStage = kP + kB;
+  constexpr int NB = JT <= 2 ? 1 : JT / 2;  // copies of B a wave and chunk
+  constexpr int NC = 4 + NB;
+  constexpr int NS = 4;                     // stores a wave and chunk
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PD * kStage + 1024];
+  __shared__ uint32_t sc[kManyTok][kManyRange / 4];
+  const Fp8FormParams& p = L.p;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = lane & 15, g = lane >> 4;
+  const int split = __builtin_amdgcn_readfirstlane((int)blockIdx.x / L.ttiles);
+  const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)blockIdx.x - split * L.ttiles) * kManyTok;
+  const int c_begin = split * L.chunks_per_split;  // a multiple of four
+  const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
+  const int n = c_end - c_begin;
+
+  const dma::v4i_t rp = dma::rsrc(p.dY + t0 * p.N, (p.T - t0) * p.N * 2), rb = dma::rsrc(p.B, p.N * p.r * 2);
+  // (without codes an empty range, which drops the stores)
+  const __amdgpu_buffer_rsrc_t rc = buf(p.codes + t0 * p.N, p.codes ? (p.T - t0) * p.N : 0);
+  const uint32_t lds0 = LDS_ADDR(lds);
+  auto issue = [&](int c) {
+    const bool in = c < n;
+    const uint32_t st = lds0 + (uint32_t)(c % PD * kStage);
+    const int64_t n0 = (int64_t)(c_begin + c) * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // rows 16 w + 4 j .. +3: piece of row R at piece ^ R % 16
+      const int R = 16 * wave + 4 * j + (lane >> 4);
+      const int64_t col = n0 + 8 * (i ^ (R & 15));
+      dma::copy16(rp, in && t0 + R < p.T && col < p.N ? (uint32_t)((R * p.N + col) * 2) : dma::kOob,
+                  st + 4096 * wave + 1024 * j);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int blk = NB * wave + j;
+      const int R = blk * (64 / PPR) + lane / PPR;
+      const int col = 8 * ((lane & (PPR - 1)) ^ tr_swz(R, PPR));
+      // with 16 columns the last waves have nothing to copy, as above
+      const bool mine = blk < 4 * JT;
+      dma::copy16(rb, in && mine && n0 + R < p.N && col < p.r ? (uint32_t)(((n0 + R) * p.r + col) * 2) : dma::kOob,
+                  mine ? st + kP + 1024 * blk : lds0 + PD * kStage);
+    }
+  };
+
+  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) (&sc[0][0])[e] = 0x7F7F7F7Fu;
+  f32x4_t acc[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < PD - 1; ++c) issue(c);
+  const int R = 16 * wave + i;
+  for (int c = 0; c < n; ++c) {
+    // this wave's copies of chunk c have landed; behind them went out those of
+    // the next PD - 2 chunks and, from the third chunk on, two chunks' stores
+    if (c >= PD - 1) dma::wait_vm<(PD - 2) * NC + (PD - 1) * NS>();
+    else dma::wait_vm<(PD - 2) * NC>();
+    lds_barrier();  // everybody's have, and chunk c - 1 is read
+    issue(c + PD - 1);
+    const uint8_t* P = lds + c % PD * kStage;
+    const uint16_t* B = reinterpret_cast<const uint16_t*>(P + kP);
+    u32x4_t x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const u32x4_t*>(P + R * 256 + (((4 * q + g) ^ i) << 4));
+    uint32_t m = absmax_bf16(16, [&](int q) -> uint32_t { return x[q >> 2][q & 3]; });
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bf16x8_t xa = __builtin_bit_cast(bf16x8_t, x[q]);
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) acc[jt] = mfma16(xa, tr_frag_swz(B, QLD, 32 * q + 8 * g, 16 * jt), acc[jt]);
+    }
+    const uint32_t m16 = (uint32_t)__shfl_xor((int)m, 16);
+    m = m16 > m ? m16 : m;
+    const uint32_t m32 = (uint32_t)__shfl_xor((int)m, 32);
+    m = m32 > m ? m32 : m;
+    const uint32_t e = scale_byte(m);
+    if (g == 0) reinterpret_cast<uint8_t*>(sc[R])[c] = (uint8_t)e;
+    const int64_t n0 = (int64_t)(c_begin + c) * 128 + 8 * g;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t col = n0 + 32 * q;
+      __builtin_amdgcn_raw_buffer_store_b64(codes8_bf16(x[q][0], x[q][1], x[q][2], x[q][3], e), rc,
+                                            t0 + R < p.T && col < p.N ? (uint32_t)(R * p.N + col) : dma::kOob, 0, 0);
+    }
+  }
+  dma::wait_vm<0>();  // no copy may land in LDS that is no longer this workgroup's
+  lds_barrier();
+
+  // whole dwords of scales, the row's padding in the last
+  const int64_t lds_ = fp8_scale_ld(p.N);
+  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) {
+    const int t = e / (kManyRange / 4), d = e % (kManyRange / 4);
+    if (p.codes && t0 + t < p.T && 4 * d < n) reinterpret_cast<uint32_t*>(p.scales + (t0 + t) * lds_ + c_begin)[d] = sc[t][d];
+  }
+  // lane l, value v: token 16 w + 4 (l/16) + v, column 16 jt + l % 16
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t t = t0 + 16 * wave + 4 * g + v;
+    if (t >= p.T) continue;
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const int j = 16 * jt + i;
+      if (j < p.r) p.part[((int64_t)split * p.T + t) * p.r + j] = acc[jt][v];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -455,6 +590,39 @@ hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream) {
   KernelEvents ev(KID_REDUCE);
   hipExtLaunchKernelGGL(k_fp8_down_sum, dim3((unsigned)((p.T * p.ldh + 255) / 256)), dim3(256), 0, stream, ev.start(),
                         ev.stop(), 0, L);
+  return hipGetLastError();
+}
+
+bool fp8_form_ok(int64_t T, int r) { return T >= kDownManyT && r > 0 && r <= 64 && r % 8 == 0; }
+
+size_t fp8_form_part_bytes(int64_t T, int64_t N, int r) {
+  int32_t per;
+  return (size_t)down_ranges(T, N, per) * T * r * 4;
+}
+
+hipError_t launch_fp8_form(const Fp8FormParams& p, hipStream_t stream) {
+  if (!fp8_form_ok(p.T, p.r) || !p.part || p.part_bytes < fp8_form_part_bytes(p.T, p.N, p.r)) return hipErrorInvalidValue;
+  FormLaunch L{};
+  L.p = p;
+  L.chunks = (int32_t)((p.N + 127) / 128);
+  DownLaunch S{};
+  S.nsplit = down_ranges(p.T, p.N, L.chunks_per_split);
+  S.p.T = p.T; S.p.r = p.r; S.p.s = p.s; S.p.U = p.G; S.p.Us = p.Gs; S.p.ldh = p.ldh; S.p.part = p.part;
+  L.ttiles = (int32_t)((p.T + kManyTok - 1) / kManyTok);
+  {
+    KernelEvents ev(KID_LORA_G);
+    const hipEvent_t e0 = ev.start(), e1 = ev.stop();
+    const dim3 grid((unsigned)(L.ttiles * S.nsplit)), block(512);
+    const int jt = (p.r + 15) / 16;
+    if (jt == 1) hipExtLaunchKernelGGL(k_fp8_form<1>, grid, block, 0, stream, e0, e1, 0, L);
+    else if (jt == 2) hipExtLaunchKernelGGL(k_fp8_form<2>, grid, block, 0, stream, e0, e1, 0, L);
+    else hipExtLaunchKernelGGL(k_fp8_form<4>, grid, block, 0, stream, e0, e1, 0, L);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  KernelEvents ev(KID_REDUCE);
+  hipExtLaunchKernelGGL(k_fp8_down_sum, dim3((unsigned)((p.T * p.ldh + 255) / 256)), dim3(256), 0, stream, ev.start(),
+                        ev.stop(), 0, S);
   return hipGetLastError();
 }
 

@@ -276,6 +276,31 @@ def test_what_is_not_finite_stays_in_its_token(T):
     assert Y2[3].isnan().all() and U2[3].isnan().all()
 
 
+@pytest.mark.parametrize("T,N,r", [(300, 320, 8), (600, 448, 8), (600, 1088, 24), (777, 576, 64)])
+def test_form_of_dy_is_the_quantizers(T, N, r):
+    """With A = 0 the adapter adds zeros to dX: whichever kernel writes the 8-bit form of dY beside G, dX has the bits
+    of the base alone.  dY with rows of zeros, blocks of subnormal and of very large values, infinities and a NaN."""
+    import torch
+    q = _q()
+    inp = _layer(N, 320, T, r, seed=N + T)
+    forms, _, _ = _forms(inp)
+    A, B, dY = dev_bf16(inp["A"]) * 0, dev_bf16(inp["B"]), dev_bf16(inp["dY"])
+    dY *= torch.exp2(torch.randint(-30, 30, (T, 1), device="cuda").float()).to(torch.bfloat16)
+    dY[5:9] = 0
+    dY[9, :128] *= 1e-39
+    dY[10, 128:256] = dY[10, 128:256].sign() * 2.0 ** 100
+    base, _, _ = q.qlora_fp8_linear_bwd(*forms, None, None, 1.0, dY)
+    dX, _, _ = q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY)
+    assert base.isfinite().all() and torch.equal(dX, base)
+    dY[3, 70], dY[T - 1, N - 1], dY[200, 0] = float("inf"), float("nan"), float("-inf")
+    dX2, _, _ = q.qlora_fp8_linear_bwd(*forms, A, B, 16.0, dY)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    for t in (3, 200, T - 1):
+        assert dX2[t].isnan().all()
+        keep[t] = False
+    assert torch.equal(dX2[keep], base[keep])
+
+
 def test_rows_behind_the_last_token_stay():
     """Outputs given as the first rows of larger buffers: what lies behind is left as it was."""
     import torch

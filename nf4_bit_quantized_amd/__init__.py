@@ -14,6 +14,7 @@ the same sources with host-side sanitizers).
 """
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -215,7 +216,7 @@ def _check_out(t, shape, dtype, name: str):
     """A caller-given output: contiguous, of the shape and dtype the call writes."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
@@ -225,7 +226,7 @@ def _check_in(t, shape, dtype, name: str):
     weight's shape, so a smaller tensor would be read past its end."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
@@ -714,18 +715,18 @@ class _LaunchOn:
 
 def _one_device(name: str, *tensors):
     """The GPU that every given tensor is on (None entries are left out)."""
-    device = None
+    first = index = None
     for t in tensors:
         if t is None:
             continue
-        d = t.device
-        if d.type != "cuda":
-            raise ValueError(f"{name}: tensors must be on the GPU")
-        if device is None:
-            device = d
-        elif d != device:
-            raise ValueError(f"{name}: the tensors are on different devices: {device} and {d}")
-    return device
+        i = t.get_device()      # an int, -1 on the CPU: a device object costs as much as the rest of a check
+        if i != index:
+            if i < 0:
+                raise ValueError(f"{name}: tensors must be on the GPU")
+            if first is not None:
+                raise ValueError(f"{name}: the tensors are on different devices: {first.device} and {t.device}")
+            first, index = t, i
+    return first.device
 
 
 def _scales_shape(rows: int, cols: int, block_rows: int):
@@ -745,11 +746,15 @@ def _check_form(codes, scales, block_rows: int, name: str):
     import torch
     if codes is None or scales is None:
         raise ValueError(f"{name}: codes and scales are required")
-    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
+    shape = codes.shape
+    if codes.dtype != torch.uint8 or len(shape) != 2 or not codes.is_contiguous():
         raise ValueError(f"{name}: codes must be a contiguous 2-D uint8 tensor")
     if block_rows not in (1, FP8_BLOCK):
         raise ValueError(f"{name}: block_rows must be 1 or {FP8_BLOCK}")
-    _check_in(scales, _scales_shape(codes.shape[0], codes.shape[1], block_rows), torch.uint8, f"{name}: scales")
+    want = _scales_shape(shape[0], shape[1], block_rows)
+    if scales.shape != want or scales.dtype != torch.uint8 or not scales.is_contiguous():
+        raise ValueError(f"{name}: scales must be a contiguous uint8 tensor of shape {want}, "
+                         f"got {scales.dtype} {tuple(scales.shape)}")
 
 
 def qlora_quantize_fp8(M, block_rows: int = 1, codes=None, scales=None, stream=None):
@@ -798,18 +803,19 @@ def qlora_dequantize_fp8(codes, scales, block_rows: int = 1, M_hat=None, stream=
     return M_hat
 
 
-def qlora_fp8_fwd_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+@functools.lru_cache(maxsize=256)      # the sizes decide it
+def _fp8_workspace_bytes(query: str, d_out: int, d_in: int, T: int, r: int) -> int:
     n = ctypes.c_size_t()
-    _check(lib().qlora_fp8_fwd_workspace_bytes(int(d_out), int(d_in), int(T), int(r), ctypes.byref(n)),
-           "qlora_fp8_fwd_workspace_bytes")
+    _check(getattr(lib(), query)(d_out, d_in, T, r, ctypes.byref(n)), query)
     return n.value
+
+
+def qlora_fp8_fwd_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+    return _fp8_workspace_bytes("qlora_fp8_fwd_workspace_bytes", int(d_out), int(d_in), int(T), int(r))
 
 
 def qlora_fp8_bwd_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
-    n = ctypes.c_size_t()
-    _check(lib().qlora_fp8_bwd_workspace_bytes(int(d_out), int(d_in), int(T), int(r), ctypes.byref(n)),
-           "qlora_fp8_bwd_workspace_bytes")
-    return n.value
+    return _fp8_workspace_bytes("qlora_fp8_bwd_workspace_bytes", int(d_out), int(d_in), int(T), int(r))
 
 
 def qlora_fp8_linear_fwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: float, Y=None, U_out=None,
@@ -829,7 +835,7 @@ def qlora_fp8_linear_fwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: floa
     _check_out(Y, (T, d_out), torch.bfloat16, "Y")
     _check_out(U_out, (T, r), torch.float32, "U_out")
     device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, Y, U_out, workspace)
-    nbytes = qlora_fp8_fwd_workspace_bytes(d_out, d_in, T, r)
+    nbytes = _fp8_workspace_bytes("qlora_fp8_fwd_workspace_bytes", d_out, d_in, T, r)
     with _LaunchOn(device, stream, name) as st:
         if Y is None:
             Y = torch.empty((T, d_out), dtype=torch.bfloat16, device=device)
@@ -872,7 +878,7 @@ def qlora_fp8_linear_bwd(W_codes, W_scales, X_codes, X_scales, A, B, alpha: floa
     _check_out(U_in, (T, r), torch.float32, "U_in")
     _grad_buffers(dX, dA, dB, T, d_out, d_in, r, accumulate)
     device = _one_device(name, W_codes, W_scales, X_codes, X_scales, A, B, dY, U_in, dX, dA, dB, workspace)
-    nbytes = qlora_fp8_bwd_workspace_bytes(d_out, d_in, T, r)
+    nbytes = _fp8_workspace_bytes("qlora_fp8_bwd_workspace_bytes", d_out, d_in, T, r)
     with _LaunchOn(device, stream, name) as st:
         if dX is None and want_dx:
             dX = torch.empty((T, d_in), dtype=torch.bfloat16, device=device)

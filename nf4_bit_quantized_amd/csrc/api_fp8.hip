@@ -84,7 +84,7 @@ Fp8BwdWs plan_bwd(int64_t N, int64_t K, int64_t T, int32_t r, void* ws) {
       if (T > kFp8FewT) w.Ap = static_cast<uint16_t*>(c.take((size_t)K * hilo_ld(r) * 2));
       w.part_bytes = std::max(std::max(w.part_bytes, fp8_down_part_bytes(T, K, r)),
                               std::max(lora_g_part_bytes(T, N, r), fp8_grad_part_bytes(T, K, N, r)));
-      if (fp8_form_ok(T, r)) w.part_bytes = std::max(w.part_bytes, fp8_form_part_bytes(T, N, r));
+      if (fp8_form_ok(r)) w.part_bytes = std::max(w.part_bytes, fp8_form_part_bytes(T, N, r));
     }
     w.part = static_cast<float*>(c.take(w.part_bytes));
   }
@@ -207,7 +207,7 @@ int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
   }
   const float s = r > 0 ? alpha / (float)r : 0.0f;
   const int64_t ldh = hilo_ld(r);
-  const bool form = fp8_form_ok(T, r);  // G and, for dX, the 8-bit form of dY from one pass over it
+  const bool form = fp8_form_ok(r);  // G and, for dX, the 8-bit form of dY from one pass over it
   const float* U = U_in;
   if (r > 0) {
     if (!U) {

@@ -89,7 +89,7 @@ struct Fp8FormParams {
   float* part;
   size_t part_bytes;
 };
-bool fp8_form_ok(int64_t T, int r);
+bool fp8_form_ok(int r);
 size_t fp8_form_part_bytes(int64_t T, int64_t N, int r);
 hipError_t launch_fp8_form(const Fp8FormParams& p, hipStream_t stream);
 

@@ -242,7 +242,8 @@ int down_ranges(int64_t T, int64_t K, int32_t& per) {
 //
 // Bound by HBM's latency: 4096 x 8192, r = 64 (101 MB read and written): 24 us,
 // 4.2 TB/s, against 16 + 16 for G and the form in launches of their own, which
-// read dY twice; a backward at 512 to 4096 tokens takes 1 to 5% less.  Vector
+// read dY twice; a whole backward takes 1 to 10% less, from 4 tokens (27.7 us
+// against 30.8, 4096 x 4096, r = 16) to 4096 (291 against 296).  Vector
 // work (the largest value and the codes on 16 bits instead of 32) and the order
 // of the chunks (other ranges' tiles starting at other columns) changed nothing.
 // ---------------------------------------------------------------------------
@@ -593,7 +594,7 @@ hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-bool fp8_form_ok(int64_t T, int r) { return T >= kDownManyT && r > 0 && r <= 64 && r % 8 == 0; }
+bool fp8_form_ok(int r) { return r > 0 && r <= 64 && r % 8 == 0; }
 
 size_t fp8_form_part_bytes(int64_t T, int64_t N, int r) {
   int32_t per;
@@ -601,7 +602,7 @@ size_t fp8_form_part_bytes(int64_t T, int64_t N, int r) {
 }
 
 hipError_t launch_fp8_form(const Fp8FormParams& p, hipStream_t stream) {
-  if (!fp8_form_ok(p.T, p.r) || !p.part || p.part_bytes < fp8_form_part_bytes(p.T, p.N, p.r)) return hipErrorInvalidValue;
+  if (!fp8_form_ok(p.r) || !p.part || p.part_bytes < fp8_form_part_bytes(p.T, p.N, p.r)) return hipErrorInvalidValue;
   FormLaunch L{};
   L.p = p;
   L.chunks = (int32_t)((p.N + 127) / 128);

@@ -20,7 +20,6 @@ namespace {
 
 using fp8::absmax_bf16;
 using fp8::codes8_bf16;
-using fp8::down_tile;
 using fp8::mfma16;
 using fp8::restore8;
 using fp8::scale_byte;
@@ -35,11 +34,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf(const void* p, int64_t byt
 }
 
 // ---------------------------------------------------------------------------
-// down: the tile is formed by down_tile (fp8_down.hpp)
+// down
+//
+// A workgroup of eight waves owns 128 tokens and all of U's columns (16 JT) for
+// one range of the contraction, a chunk of 128 positions at a time: X's codes
+// [128][128 B] and A's rows [16 JT][256 B] are copied straight into one of PD
+// LDS stages, PD - 1 chunks ahead; wave w multiplies tokens 16 w .. +15.  The
+// range's scales (at most 32 chunks) are in LDS from the start, so nothing but
+// the copies is in flight in the loop; as many ranges as fill the CUs, of at most
+// 32 chunks (whole dwords of scales), whose sums k_fp8_down_sum adds.  Tiles of 16
+// x 16 with fragments loaded from global memory, which cost 64 cache lookups a
+// load, took 18 us at 4096 x 8192, r = 64, against 13 here (33.5 MB of codes),
+// and 15 to 34 with no second launch at 129 to 500 tokens, against 6 to 13 and
+// about 4 for the sums.
 // ---------------------------------------------------------------------------
 struct DownLaunch {
   Fp8DownParams p;
-  int32_t ttiles, jtiles, nsplit;
+  int32_t ttiles, nsplit;
   int32_t chunks, chunks_per_split;
 };
 
@@ -57,50 +68,6 @@ __device__ __forceinline__ void down_out(const Fp8DownParams& p, int64_t t, int 
   if (p.Us) p.Us[t * p.ldh + c] = h;
 }
 
-// A workgroup owns 16 RT tokens and 16 JT columns of U for one range of the
-// contraction; its NW waves take the range's chunks in turn and add their tiles
-// in LDS in wave order.
-template <int RT, int JT, int NW>
-__global__ __launch_bounds__(NW * 64) void k_fp8_down(DownLaunch L) {
-  constexpr int TOK = 16 * RT, COL = 16 * JT, LD = COL + 1;
-  __shared__ float red[NW][TOK][LD];
-  const Fp8DownParams& p = L.p;
-  int b = (int)blockIdx.x;
-  const int split = b / (L.ttiles * L.jtiles);
-  b -= split * (L.ttiles * L.jtiles);
-  const int64_t t0 = (int64_t)(b / L.jtiles) * TOK;
-  const int j0 = (b % L.jtiles) * COL;
-  const int c_begin = split * L.chunks_per_split;
-  const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
-  down_tile<RT, JT, NW, LD>(p, t0, j0, c_begin, c_end, __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), red);
-  __syncthreads();
-  auto sum = [&](int rr, int j) {
-    float v = red[0][rr][j];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v += red[w][rr][j];
-    return v;
-  };
-  // this workgroup's columns of U, their hi and lo columns of Us, and (its
-  // share of) the padding
-  for (int e = threadIdx.x; e < TOK * COL; e += NW * 64) {
-    const int rr = e / COL, j = j0 + e % COL;
-    const int64_t t = t0 + rr;
-    if (t >= p.T) continue;
-    if (j < p.r) {
-      const float v = sum(rr, j - j0);
-      if (p.U) p.U[t * p.r + j] = v;
-      if (p.Us) {
-        uint16_t hi, lo;
-        split_bf16(p.s * v, hi, lo);
-        p.Us[t * p.ldh + j] = hi;
-        p.Us[t * p.ldh + p.r + j] = lo;
-      }
-    }
-    if (p.Us)
-      for (int64_t c = 2 * p.r + j; c < p.ldh; c += COL * L.jtiles) p.Us[t * p.ldh + c] = 0;
-  }
-}
-
 __global__ __launch_bounds__(256) void k_fp8_down_sum(DownLaunch L) {
   const Fp8DownParams& p = L.p;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -111,41 +78,29 @@ __global__ __launch_bounds__(256) void k_fp8_down_sum(DownLaunch L) {
   });
 }
 
-// ---------------------------------------------------------------------------
-// down for many tokens
-//
-// A workgroup of eight waves owns 128 tokens and all of U's columns (16 JT) for
-// one range of the contraction, a chunk of 128 positions at a time: X's codes
-// [128][128 B] and A's rows [16 JT][256 B] are copied straight into one of PD
-// LDS stages, PD - 1 chunks ahead; wave w multiplies tokens 16 w .. +15.  The
-// range's scales (at most 32 chunks) are in LDS from the start, so nothing but
-// the copies is in flight in the loop.  Fragments loaded from global memory (the
-// tiles above) cost 64 cache lookups a load: 18 us at 4096 x 8192, r = 64,
-// against 13 here (33.5 MB of codes).
-// ---------------------------------------------------------------------------
-constexpr int kManyTok = 128;
-constexpr int kManyRange = 32;  // chunks of a range at most
+constexpr int kDownTok = 128;
+constexpr int kDownRange = 32;  // chunks of a range at most
 
 template <int JT>
-__global__ __launch_bounds__(512) void k_fp8_down_many(DownLaunch L) {
+__global__ __launch_bounds__(512) void k_fp8_down(DownLaunch L) {
   constexpr int PD = JT <= 4 ? 4 : 3;
-  constexpr int kX = kManyTok * 128, kA = 16 * JT * 256, kStage = kX + kA;
+  constexpr int kX = kDownTok * 128, kA = 16 * JT * 256, kStage = kX + kA;
   constexpr int NA = JT <= 2 ? 1 : JT / 2;  // copies of A a wave and chunk
   constexpr int NC = 2 + NA;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[PD * kStage + 1024];
-  __shared__ uint32_t sc[kManyTok][kManyRange / 4];
+  __shared__ uint32_t sc[kDownTok][kDownRange / 4];
   const Fp8DownParams& p = L.p;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int i = lane & 15, g = lane >> 4;
   const int split = (int)blockIdx.x / L.ttiles;
-  const int64_t t0 = (int64_t)((int)blockIdx.x - split * L.ttiles) * kManyTok;
+  const int64_t t0 = (int64_t)((int)blockIdx.x - split * L.ttiles) * kDownTok;
   const int c_begin = split * L.chunks_per_split;  // a multiple of four
   const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
   const int64_t ldx = fp8_scale_ld(p.K);
 
-  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) {
-    const int t = e / (kManyRange / 4), d = e % (kManyRange / 4);
+  for (int e = threadIdx.x; e < kDownTok * (kDownRange / 4); e += 512) {
+    const int t = e / (kDownRange / 4), d = e % (kDownRange / 4);
     uint32_t v = 0x7F7F7F7Fu;
     if (t0 + t < p.T && c_begin + 4 * d < c_end) v = reinterpret_cast<const uint32_t*>(p.Xs + (t0 + t) * ldx + c_begin)[d];
     sc[t][d] = v;
@@ -218,14 +173,10 @@ __global__ __launch_bounds__(512) void k_fp8_down_many(DownLaunch L) {
   }
 }
 
-// Many tokens: 128 x r tiles, the contraction in as many ranges of at most 32
-// chunks (whole dwords of scales) as fill the CUs; their sums are added by
-// k_fp8_down_sum.  Fewer: 16 x 16 tiles over the whole contraction, one launch.
-constexpr int64_t kDownManyT = 512;
 int down_ranges(int64_t T, int64_t K, int32_t& per) {
-  const int64_t tiles = (T + kManyTok - 1) / kManyTok, chunks = (K + 127) / 128;
+  const int64_t tiles = (T + kDownTok - 1) / kDownTok, chunks = (K + 127) / 128;
   int64_t s = 256 / tiles;
-  if (s < (chunks + kManyRange - 1) / kManyRange) s = (chunks + kManyRange - 1) / kManyRange;
+  if (s < (chunks + kDownRange - 1) / kDownRange) s = (chunks + kDownRange - 1) / kDownRange;
   per = (int32_t)(((chunks + s - 1) / s + 3) / 4 * 4);
   return (int)((chunks + per - 1) / per);
 }
@@ -233,7 +184,7 @@ int down_ranges(int64_t T, int64_t K, int32_t& per) {
 // ---------------------------------------------------------------------------
 // form: G and the 8-bit form of dY in one pass over it
 //
-// As down for many tokens: a workgroup of eight waves owns 128 tokens for one
+// As down: a workgroup of eight waves owns 128 tokens for one
 // range of the contraction, a chunk of 128 columns at a time, dY's [128][256 B]
 // and B's [128][32 JT B] copied into LDS two chunks ahead.  A lane holds 32
 // columns of one row, its share of four MFMAs; four lanes have the row's block
@@ -256,18 +207,18 @@ template <int JT>
 __global__ __launch_bounds__(512) void k_fp8_form(FormLaunch L) {
   constexpr int PD = 3;
   constexpr int QLD = 16 * JT, PPR = 2 * JT;  // a row of B: elements, 16-byte pieces
-  constexpr int kP = kManyTok * 256, kB = 128 * QLD * 2, kStage = kP + kB;
+  constexpr int kP = kDownTok * 256, kB = 128 * QLD * 2, kStage = kP + kB;
   constexpr int NB = JT <= 2 ? 1 : JT / 2;  // copies of B a wave and chunk
   constexpr int NC = 4 + NB;
   constexpr int NS = 4;                     // stores a wave and chunk
   __shared__ __attribute__((aligned(1024))) uint8_t lds[PD * kStage + 1024];
-  __shared__ uint32_t sc[kManyTok][kManyRange / 4];
+  __shared__ uint32_t sc[kDownTok][kDownRange / 4];
   const Fp8FormParams& p = L.p;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int i = lane & 15, g = lane >> 4;
   const int split = __builtin_amdgcn_readfirstlane((int)blockIdx.x / L.ttiles);
-  const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)blockIdx.x - split * L.ttiles) * kManyTok;
+  const int64_t t0 = (int64_t)__builtin_amdgcn_readfirstlane((int)blockIdx.x - split * L.ttiles) * kDownTok;
   const int c_begin = split * L.chunks_per_split;  // a multiple of four
   const int c_end = c_begin + L.chunks_per_split < L.chunks ? c_begin + L.chunks_per_split : L.chunks;
   const int n = c_end - c_begin;
@@ -299,7 +250,7 @@ __global__ __launch_bounds__(512) void k_fp8_form(FormLaunch L) {
     }
   };
 
-  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) (&sc[0][0])[e] = 0x7F7F7F7Fu;
+  for (int e = threadIdx.x; e < kDownTok * (kDownRange / 4); e += 512) (&sc[0][0])[e] = 0x7F7F7F7Fu;
   f32x4_t acc[JT];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -344,8 +295,8 @@ __global__ __launch_bounds__(512) void k_fp8_form(FormLaunch L) {
 
   // whole dwords of scales, the row's padding in the last
   const int64_t lds_ = fp8_scale_ld(p.N);
-  for (int e = threadIdx.x; e < kManyTok * (kManyRange / 4); e += 512) {
-    const int t = e / (kManyRange / 4), d = e % (kManyRange / 4);
+  for (int e = threadIdx.x; e < kDownTok * (kDownRange / 4); e += 512) {
+    const int t = e / (kDownRange / 4), d = e % (kDownRange / 4);
     if (p.codes && t0 + t < p.T && 4 * d < n) reinterpret_cast<uint32_t*>(p.scales + (t0 + t) * lds_ + c_begin)[d] = sc[t][d];
   }
   // lane l, value v: token 16 w + 4 (l/16) + v, column 16 jt + l % 16
@@ -557,37 +508,28 @@ int grad_splits(int64_t T, int64_t K, int64_t N) {
 
 size_t fp8_down_part_bytes(int64_t T, int64_t K, int r) {
   int32_t per;
-  return T < kDownManyT ? 0 : (size_t)down_ranges(T, K, per) * T * r * 4;
+  return (size_t)down_ranges(T, K, per) * T * r * 4;
 }
 
 hipError_t launch_fp8_down(const Fp8DownParams& p, hipStream_t stream) {
+  if (!p.part || p.part_bytes < fp8_down_part_bytes(p.T, p.K, p.r)) return hipErrorInvalidValue;
   DownLaunch L{};
   L.p = p;
   L.chunks = (int32_t)((p.K + 127) / 128);
-  const int jt = (p.r + 15) / 16;
-  const bool many = p.T >= kDownManyT;
-  if (many && (!p.part || p.part_bytes < fp8_down_part_bytes(p.T, p.K, p.r))) return hipErrorInvalidValue;
+  L.nsplit = down_ranges(p.T, p.K, L.chunks_per_split);
+  L.ttiles = (int32_t)((p.T + kDownTok - 1) / kDownTok);
   {
     KernelEvents ev(KID_FP8_DOWN);
     const hipEvent_t e0 = ev.start(), e1 = ev.stop();
-    if (!many) {
-      L.nsplit = 1;
-      L.chunks_per_split = L.chunks;
-      L.ttiles = (int32_t)((p.T + 15) / 16);
-      L.jtiles = jt;
-      hipExtLaunchKernelGGL((k_fp8_down<1, 1, 16>), dim3((unsigned)(L.ttiles * L.jtiles)), dim3(1024), 0, stream, e0, e1, 0, L);
-    } else {
-      L.nsplit = down_ranges(p.T, p.K, L.chunks_per_split);
-      L.ttiles = (int32_t)((p.T + kManyTok - 1) / kManyTok);
-      const dim3 grid((unsigned)(L.ttiles * L.nsplit)), block(512);
-      if (jt == 1) hipExtLaunchKernelGGL(k_fp8_down_many<1>, grid, block, 0, stream, e0, e1, 0, L);
-      else if (jt == 2) hipExtLaunchKernelGGL(k_fp8_down_many<2>, grid, block, 0, stream, e0, e1, 0, L);
-      else if (jt <= 4) hipExtLaunchKernelGGL(k_fp8_down_many<4>, grid, block, 0, stream, e0, e1, 0, L);
-      else hipExtLaunchKernelGGL(k_fp8_down_many<8>, grid, block, 0, stream, e0, e1, 0, L);
-    }
+    const dim3 grid((unsigned)(L.ttiles * L.nsplit)), block(512);
+    const int jt = (p.r + 15) / 16;
+    if (jt == 1) hipExtLaunchKernelGGL(k_fp8_down<1>, grid, block, 0, stream, e0, e1, 0, L);
+    else if (jt == 2) hipExtLaunchKernelGGL(k_fp8_down<2>, grid, block, 0, stream, e0, e1, 0, L);
+    else if (jt <= 4) hipExtLaunchKernelGGL(k_fp8_down<4>, grid, block, 0, stream, e0, e1, 0, L);
+    else hipExtLaunchKernelGGL(k_fp8_down<8>, grid, block, 0, stream, e0, e1, 0, L);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !many) return e;
+  if (e != hipSuccess) return e;
   KernelEvents ev(KID_REDUCE);
   hipExtLaunchKernelGGL(k_fp8_down_sum, dim3((unsigned)((p.T * p.ldh + 255) / 256)), dim3(256), 0, stream, ev.start(),
                         ev.stop(), 0, L);
@@ -609,7 +551,7 @@ hipError_t launch_fp8_form(const Fp8FormParams& p, hipStream_t stream) {
   DownLaunch S{};
   S.nsplit = down_ranges(p.T, p.N, L.chunks_per_split);
   S.p.T = p.T; S.p.r = p.r; S.p.s = p.s; S.p.U = p.G; S.p.Us = p.Gs; S.p.ldh = p.ldh; S.p.part = p.part;
-  L.ttiles = (int32_t)((p.T + kManyTok - 1) / kManyTok);
+  L.ttiles = (int32_t)((p.T + kDownTok - 1) / kDownTok);
   {
     KernelEvents ev(KID_LORA_G);
     const hipEvent_t e0 = ev.start(), e1 = ev.stop();

@@ -465,7 +465,7 @@ __global__ __launch_bounds__(256, 2) void k_fp8_few(FewLaunch L) {
   const int c_begin = range * L.chunks_per_range;
   const int c_end = c_begin + L.chunks_per_range < L.chunks ? c_begin + L.chunks_per_range : L.chunks;
   float(*red)[16][17] = reinterpret_cast<float(*)[16][17]>(lds);
-  fp8::down_tile<1, 1, 4, 17>(L.d, t0, j0, c_begin, c_end, __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), red);
+  fp8::down_tile<4, 17>(L.d, t0, j0, c_begin, c_end, __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), red);
   __syncthreads();
   const int rr = threadIdx.x >> 4, j = threadIdx.x & 15;
   if (t0 + rr < L.d.T && j0 + j < L.d.r)

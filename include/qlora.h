@@ -464,7 +464,9 @@ int qlora_fp8_linear_bwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
  * by qlora_linear_bwd (it does not depend on X).  accumulate, T == 0, r == 0
  * and dX == NULL as for qlora_fp8_linear_bwd.  There is no form of this call
  * with LoRA dropout or over several layers.
- * Errors: as qlora_linear_bwd; the workspace is 16-byte aligned.
+ * Errors: as qlora_linear_bwd, and SHAPE (from the workspace query too) where
+ * A (r*K*2 bytes) or B (r*N*2) is not below 2^31 - 16 bytes; the workspace is
+ * 16-byte aligned.
  */
 int qlora_checkpoint_workspace_bytes(const qlora_nf4_desc* d, int64_t T, int32_t r, size_t* bytes);
 int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, const uint8_t* codes,

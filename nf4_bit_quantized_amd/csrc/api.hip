@@ -829,6 +829,15 @@ struct CheckpointWs {
   size_t bytes = 0;
 };
 
+// The layer's limits, and A's and B's own: the kernels that read the
+// checkpoint address them with 32-bit offsets too.
+static int check_checkpoint(const qlora_nf4_desc* d, int64_t T, int32_t r) {
+  const int st = check_layer(d, T, r);
+  if (st) return st;
+  if (r * d->d_in * 2 > kMaxOperandBytes || r * d->d_out * 2 > kMaxOperandBytes) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
 static CheckpointWs plan_checkpoint(const qlora_nf4_desc* d, int64_t T, int32_t r, void* ws) {
   CheckpointWs w;
   Carve c(ws);
@@ -847,7 +856,7 @@ static CheckpointWs plan_checkpoint(const qlora_nf4_desc* d, int64_t T, int32_t 
 
 int qlora_checkpoint_workspace_bytes(const qlora_nf4_desc* d, int64_t T, int32_t r, size_t* bytes) {
   if (!bytes) return QLORA_ERR_NULL;
-  const int st = check_layer(d, T, r);
+  const int st = check_checkpoint(d, T, r);
   if (st) return st;
   *bytes = plan_checkpoint(d, T, r, nullptr).bytes;
   return QLORA_OK;
@@ -858,7 +867,7 @@ int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, 
                                 int32_t r, float alpha, const uint16_t* A, const uint16_t* B, const float* U_in,
                                 const uint16_t* dY, uint16_t* dX, float* dA, float* dB, int32_t accumulate,
                                 void* workspace, size_t workspace_bytes, void* stream) {
-  const int st = check_layer(d, T, r);
+  const int st = check_checkpoint(d, T, r);
   if (st) return st;
   if (!packed || (!codes && d->dq_blocksize) || !consts) return QLORA_ERR_NULL;
   if (T > 0 && (!dY || (r > 0 && (!X_codes || !X_scales)))) return QLORA_ERR_NULL;

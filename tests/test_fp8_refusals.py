@@ -127,6 +127,23 @@ def test_checkpoint_backward_pointers():
     assert L.qlora_checkpoint_workspace_bytes(D, 4, 8, None) == NULL
 
 
+# (d_out, d_in, r): A or B at 2^31 bytes, above it, and at 2^32, where a 32-bit offset is back at zero
+@pytest.mark.parametrize("N,K,r", [(64, 1 << 23, 128), (64, 1 << 24, 64), (64, 1 << 24, 128), (1 << 24, 64, 64),
+                                   (1 << 24, 64, 128)])
+def test_checkpoint_adapter_sizes_refused(N, K, r):
+    """The kernels address A and B with 32-bit byte offsets, whether U is given or not."""
+    L = q.lib()
+    n = ctypes.c_size_t()
+    D = ctypes.byref(q._desc(N, K))
+    assert L.qlora_checkpoint_workspace_bytes(D, 1, r, ctypes.byref(n)) == SHAPE
+    for U in (F, None):
+        assert L.qlora_linear_bwd_checkpoint(D, F, F, F, 1, F, F, r, 1.0, F, F, U, F, F, F, F, 0, F, 1 << 40, None) == SHAPE
+    # as the layer on an 8-bit weight does; and the sizes below are there
+    assert L.qlora_fp8_bwd_workspace_bytes(N, K, 1, r, ctypes.byref(n)) == SHAPE
+    D = ctypes.byref(q._desc(min(N, (1 << 23) - 64), min(K, (1 << 23) - 64)))
+    assert L.qlora_checkpoint_workspace_bytes(D, 1, r, ctypes.byref(n)) == OK
+
+
 def test_workspaces_hold_what_they_are_said_to():
     """No tokens, or no adapter where only it needs scratch: none.  Else at least the 8-bit form of dY, U and G."""
     assert q.qlora_fp8_fwd_workspace_bytes(256, 256, 0, 8) == 0

@@ -395,7 +395,8 @@ int qlora_linear_bwd_dropout(const qlora_nf4_desc* d, const uint8_t* packed, con
  * layer whose frozen weight is kept at 8 bits (block_rows 128).
  *
  * codes and M are 16-byte aligned, scales 4-byte aligned;
- * rows * ceil(cols / 512) < 2^27.
+ * rows * ceil(cols / 512) < 2^27 and rows * cols <= 2^36 - 2^12 (SHAPE
+ * otherwise).
  * Scales other than 1 .. 254 are not produced; results for them are
  * unspecified.
  */

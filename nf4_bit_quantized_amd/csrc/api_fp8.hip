@@ -15,8 +15,10 @@ namespace {
 int check_form(int64_t rows, int64_t cols, int32_t block_rows) {
   if (block_rows != 1 && block_rows != kFp8Block) return QLORA_ERR_UNSUPPORTED;
   if (rows < 0 || cols <= 0 || cols % 64 != 0 || rows >= kMaxDim || cols >= kMaxDim) return QLORA_ERR_SHAPE;
-  // units of 512 columns, 16 threads each, in a grid of fewer than 2^32 threads
+  // units of 512 columns are counted with 32 bits, sixteen threads each; the
+  // restore's threads, sixteen codes each in workgroups of 256, are fewer than 2^32
   if (rows * (fp8_scale_ld(cols) / 4) >= (int64_t)1 << 27) return QLORA_ERR_SHAPE;
+  if (rows * (cols / 16) > ((int64_t)1 << 32) - 256) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 

@@ -36,6 +36,22 @@ def test_forms_refused(rows, cols, br, status):
         assert L.qlora_dequantize_fp8(rows, cols, br, F, F, F, None) == status
 
 
+@pytest.mark.parametrize("cols,br", [(512, 1), (512, 128), (1024, 1)])
+def test_largest_forms(cols, br):
+    """What the sizes accept, every kernel can launch: sixteen codes a thread, in a grid of fewer than 2^32 threads
+    of whole workgroups of 256."""
+    L = q.lib()
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    most = ((1 << 32) - 256) * 16 // cols
+    for rows in range(most - 3, most + 4):
+        fits = -(-(rows * cols // 16) // 256) * 256 < 1 << 32
+        assert fits == (rows <= most)
+        assert L.qlora_fp8_sizes(rows, cols, br, ctypes.byref(a), ctypes.byref(b)) == (OK if fits else SHAPE)
+        if not fits:
+            assert L.qlora_quantize_fp8(rows, cols, br, F, 0, F, F, None) == SHAPE
+            assert L.qlora_dequantize_fp8(rows, cols, br, F, F, F, None) == SHAPE
+
+
 def test_form_pointers():
     L = q.lib()
     a = ctypes.c_size_t()

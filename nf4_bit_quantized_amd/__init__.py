@@ -345,6 +345,8 @@ def _workspace(nbytes: int, device, workspace=None):
     if nbytes == 0:
         return workspace
     if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small")
         return workspace

@@ -234,3 +234,16 @@ def test_binding_refuses_forms_and_host_tensors():
         q.qlora_quantize_fp8(_t((4, 64), torch.float32), codes=_t((4, 128)))
     with pytest.raises(ValueError, match="contiguous"):
         q.qlora_quantize_fp8(_t((64, 64), torch.float32).t()[:, :64].t()[::2])
+
+
+@pytest.mark.parametrize("workspace", [_t((1,)).expand(4096), _t((8192,))[::2], _t((64, 128)).t()])
+def test_binding_refuses_workspaces_with_holes(workspace):
+    """A workspace of enough elements that are not its bytes one after another: the kernels would write past or between
+    them."""
+    assert workspace.numel() >= 4096
+    with pytest.raises(ValueError, match="contiguous"):
+        q._workspace(4096, "cpu", workspace)
+    given = _t((4096,))
+    assert q._workspace(4096, "cpu", given) is given
+    with pytest.raises(ValueError, match="small"):
+        q._workspace(4097, "cpu", given)

@@ -413,7 +413,10 @@ int qlora_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const voi
 
 /*
  * codes, scales -> M_hat [rows][cols] bf16 = bf16_rne(code * 2^(e - 127)).
- * Exact wherever the value is a normal bf16 (e >= 8 suffices).  For a layer
+ * Exact for e >= 3 and |code| * 2^(e - 127) < 2^128.  With e = 1 or 2 values
+ * below bf16's least step, 2^-133, are rounded to it; and finite elements of
+ * 1.9375 * 2^127 and above have the code 256 * 2^120 = 2^128, which is restored
+ * as an infinity (here and where U, dA and dB read the form).  For a layer
  * input that is recomputed from, and for export of an 8-bit weight.
  * Errors: NULL, SHAPE, UNSUPPORTED (block_rows, alignment), HIP.
  */
@@ -427,11 +430,14 @@ int qlora_dequantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const u
  * X_hat, W_hat being the values the forms stand for.  A [r][d_in], B
  * [d_out][r], Y [T][d_out] bf16; U_out (fp32 [T][r]) may be NULL; r == 0 (A, B
  * NULL) is the base product alone.  Sums are fp32, except that the matrix
- * units add the products of eight consecutive (in their order) codes aligned
- * to the largest of the eight, which drops what is below 2^-13 of it.
+ * units add the products of eight consecutive codes aligned to the largest of
+ * the eight, which drops what is below 2^-13 of it.  s U enters its product in
+ * fp32 with at most 128 tokens, with more as two bf16 terms (16 bits).  What is
+ * not finite in the input becomes NaN in its own token's Y and U.
  * Deterministic.  Size limits, alignment and errors as qlora_linear_fwd (the
- * weight's codes in place of the packed weight; scales 4-byte aligned); the
- * workspace is 16-byte aligned.
+ * weight's codes in place of the packed weight; the rank-r pairs are [T][2r],
+ * [N][2r] and [K][2r], 2r rounded up to a multiple of 64; scales 4-byte
+ * aligned); the workspace is 16-byte aligned.
  */
 int qlora_fp8_fwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t T, int32_t r, size_t* bytes);
 int qlora_fp8_linear_fwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, const uint8_t* W_scales, int64_t T,
@@ -447,7 +453,8 @@ int qlora_fp8_linear_fwd(int64_t d_out, int64_t d_in, const uint8_t* W_codes, co
  * accumulate == 0 overwrites dA and dB, otherwise they are added to (one fp32
  * addition per element).  dX may be NULL (the first layer: adapter gradients
  * only).  U_in NULL recomputes U from X_hat.  X_codes and X_scales may be
- * NULL when r == 0.  dA and dB carry fp32 accuracy.  T == 0: dA and dB become
+ * NULL when r == 0.  dA and dB carry fp32 accuracy (G and U enter their
+ * products with 24 bits); s G enters dX as s U does Y.  T == 0: dA and dB become
  * zero, or stay as they are when accumulating.  Other arguments, limits and
  * errors as above and as qlora_linear_bwd.
  */

@@ -37,7 +37,8 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // copy in flight before each LDS read it cannot prove disjoint (draining the
 // prefetch); the kernels wait for exactly the copies they read instead, and
 // issue no compiler-visible vector-memory operation while copies are in
-// flight, so that the counts they wait on are exact.  The kernels that
+// flight, or a number of them that they count (k_fp8_form's stores), so that
+// the counts they wait on are exact.  The kernels that
 // include this file use M0 for nothing else (checked in the generated code).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"

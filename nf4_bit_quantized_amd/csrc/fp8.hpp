@@ -46,6 +46,15 @@ struct Fp8Params {
   const float* G;      // dx: fp32 [T][r]
   float* U;            // forward: receives U, or null
 };
+// The most tokens for which the product is a stream of the weight with the
+// rank-r term in the pass behind it.  Forward, this way against U's own kernel
+// and the tiles of plan_product: 4096 x 4096, r = 16: 21 us against 23 at 128
+// tokens, 21 against 24 at 160; 8192 x 8192, r = 64: 34 and 36, 38.5 and 40;
+// 11008 x 4096, r = 16: 26 and 27.5, 29 and 28.  Larger weights cross earlier:
+// 28672 x 8192, r = 64: 72 and 77 at 64 tokens, 84 and 79 at 96, 93 and 80 at
+// 128; 8192 x 28672: 69 and 72.5, 83 and 81, 86 and 81.  Whole backward passes
+// cross between 128 and 160 tokens too (8192 x 8192: 53 and 54, 60 and 59); of
+// 28672 x 8192 they are within 3% up to 96 tokens, 118 and 101 at 128.
 constexpr int64_t kFp8FewT = 128;
 size_t fp8_product_part_bytes(int64_t T, int64_t Nw, int64_t Kw, int dx, int r);
 hipError_t launch_fp8_product(const Fp8Params& p, hipStream_t stream);

@@ -16,7 +16,8 @@ __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
-// Eight codes (two dwords) restored: exact, save below bf16's own range.
+// Eight codes (two dwords) restored: exact, save below bf16's subnormal steps
+// and from 2^128 on, which is an infinity.
 __device__ __forceinline__ u32x4_t restore8(uint32_t a, uint32_t b, float k) {
   return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, false)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, k, true)),

@@ -69,8 +69,9 @@ __device__ __forceinline__ uint32_t absmax_bf16(int n, const Dword& x) {
 }
 
 // Eight codes of four dwords of bf16 values.  The instruction divides by the
-// scale and rounds once; its results are those of codes8 for every bf16 value
-// and every e (checked for all of them, what is not finite among them).
+// scale and rounds once, so its results are those of codes8 (the tests compare
+// the two forms on every finite bf16 value, in blocks of neighbours, of twenty
+// binades and of any sizes, and on what is not finite).
 __device__ __forceinline__ u32x2_t codes8_bf16(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   typedef short s16x2_t __attribute__((ext_vector_type(2)));

@@ -499,8 +499,8 @@ __global__ __launch_bounds__(256) void k_fp8_grad_sum(GradLaunch L) {
 // Token ranges: 512 workgroups in all, of four chunks each at least.  r = 64, G
 // and its sum included: 8192 x 8192, 4096 tokens: 63 us, as with 256 workgroups,
 // with 1024 79; 22016 x 8192: 121 against 132 and 131 (1333 tokens: 57.5, 55 and
-// 66).  At most 16 ranges; with 8 or 32 the times are the
-// same within a few percent.
+// 66).  At most 16 ranges; with 8 or 32 the times are the same within a few
+// percent.
 int grad_splits(int64_t T, int64_t K, int64_t N) {
   const int64_t slabs = (K + kGradM - 1) / kGradM + (N + kGradM - 1) / kGradM;
   const int64_t chunks = (T + kGradChunk - 1) / kGradChunk;

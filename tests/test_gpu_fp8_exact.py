@@ -199,3 +199,62 @@ def test_what_the_matrix_units_keep(N, T, backward):
     else:
         Y, _ = q.qlora_fp8_linear_fwd(*W, *q.qlora_quantize_fp8(_bf16(X)), None, None, 1.0)
     _same(Y, np.repeat(2.0 ** (8 - d)[:, None], N, 1), "Y")
+
+
+def _few_whole(rows, cols, seed):
+    """A matrix of whole numbers of at most 7 on the GPU, zero but for some thousands of places and its corners."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = min(rows * cols // 8, 4000)
+    M = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    i, j = (torch.randint(0, m, (n,), generator=g, device="cuda") for m in (rows, cols))
+    M[i, j] = torch.randint(-7, 8, (n,), generator=g, device="cuda").to(torch.bfloat16)
+    M[0, 0], M[0, -1], M[-1, 0], M[-1, -1] = 3.0, -5.0, 2.0, 7.0
+    return M
+
+
+def _product(a, b):
+    """a b in float64, a million rows, columns and terms at a time."""
+    import torch
+    step = 1 << 20
+    out = torch.zeros((a.shape[0], b.shape[1]), device="cuda")
+    for i in range(0, a.shape[0], step):
+        for j in range(0, b.shape[1], step):
+            for k in range(0, a.shape[1], step):
+                x = a[i:i + step, k:k + step].double().contiguous() @ b[k:k + step, j:j + step].double().contiguous()
+                out[i:i + step, j:j + step] += x.float()
+    return out
+
+
+@pytest.mark.parametrize("N,K,T,r", [
+    (64, 128, 8388000, 8),          # X and its gradient 100 KB under 2^31 bytes
+    (16777152, 64, 64, 8),          # Y and B's pair
+    (64, 16777152, 64, 8),          # X and A's pair
+    (64, 33554368, 16, 0),          # 2^31 codes of the weight, in few rows and in many
+    (33554368, 64, 16, 0),
+    (46336, 46336, 3, 8),
+])
+def test_largest_operands(N, K, T, r):
+    """Operands just under the 2^31 bytes that the kernels address, whole numbers among zeros, bit for bit."""
+    import torch
+    q = _q()
+    say(f"largest {N}x{K} T {T} r {r}")
+    W, X, dY = (_few_whole(*shape, seed) for seed, shape in enumerate(((N, K), (T, K), (T, N))))
+    A, B = (_few_whole(r, K, 3), _few_whole(N, r, 4)) if r else (None, None)
+    Wf, Xf = q.qlora_quantize_fp8(W, block_rows=128), q.qlora_quantize_fp8(X)
+    assert torch.equal(q.qlora_dequantize_fp8(*Wf, block_rows=128), W) and torch.equal(q.qlora_dequantize_fp8(*Xf), X)
+    Y, U = q.qlora_fp8_linear_fwd(*Wf, *Xf, A, B, float(max(r, 1)))
+    want = _product(X, W.T)
+    if r:
+        u = _product(X, A.T)
+        assert torch.equal(U, u)
+        want += _product(u, B.T)
+    assert want[-1, -1] != 0 and torch.equal(Y, want.to(torch.bfloat16))
+    del want, Y
+    dX, dA, dB = q.qlora_fp8_linear_bwd(*Wf, *Xf, A, B, float(max(r, 1)), dY, U_in=U)
+    want = _product(dY, W)
+    if r:
+        G = _product(dY, B)
+        want += _product(G, A)
+        assert torch.equal(dA, _product(G.T, X)) and torch.equal(dB, _product(dY.T, u))
+    assert want[-1, -1] != 0 and torch.equal(dX, want.to(torch.bfloat16))

@@ -484,6 +484,142 @@ int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, 
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The two ends of the layers
+ * --------------------------
+ * What forms a layer's input X and takes its dX back (qlora_norm_*), and what
+ * turns the last layer's Y, the logits, into a training loss and its dY or
+ * into an answer's scores (qlora_token_logprob*, qlora_distill_*): the calls
+ * between the layers of a training step ("QLoRA技术从入门到精通" §3: forward,
+ * loss, backward, update of A and B).
+ *
+ * Residual norm, per token over D channels (D a multiple of 64, at most
+ * 16384; T < 2^22):
+ *   m  = block * r_b,  r_b = 1 / sqrt(mean(block^2) + eps)
+ *   h' = h + scale * gate * post_weight * m
+ *   x  = weight * h' * r,  r = 1 / sqrt(mean(h'^2) + eps)
+ * block: a layer's output, bf16 [T][D]; NULL leaves h as it is (h_out is then
+ * not written and may be NULL).  post_weight [D] or NULL: without it there is
+ * no norm behind the block, m = block.  gate [D] or NULL (1).  stream_format:
+ * QLORA_W_F32 or QLORA_W_BF16, of h, h_out, dh_out and dh.  weight_format: the
+ * same two, of weight, post_weight and gate.  Sums and statistics are fp32; x
+ * is formed from h' before h' is rounded to the stream's type.
+ * X: bf16 [T][D] or NULL.  codes, scales: x in the 8-bit form by rows (sizes
+ * from qlora_fp8_sizes, from x in fp32), for qlora_fp8_linear_fwd; both NULL
+ * or both given; X or they are required.  stats: fp32 [T][2], (r, r_b), for
+ * the backward; r_b is 1 without a norm behind the block.
+ * h_out may be h.  Otherwise outputs must not alias inputs.  Matrices and
+ * vectors are 16-byte aligned, scales and stats 4-byte.
+ * Deterministic.  Errors: NULL (post_weight or gate without a block, too),
+ * SHAPE, UNSUPPORTED (formats, alignment, eps negative or not finite, scale
+ * not finite), HIP.
+ */
+int qlora_norm_fwd(int64_t T, int64_t D, const void* h, int32_t stream_format, const uint16_t* block,
+                   const void* weight, const void* post_weight, const void* gate, int32_t weight_format, float scale,
+                   float eps, void* h_out, uint16_t* X, uint8_t* codes, uint8_t* scales, float* stats, void* stream);
+
+/*
+ * Its backward.  dX bf16 [T][D]: the gradient of x (a layer's dX); dh_out: that
+ * of h' from everything behind it, in the stream's type, or NULL (none);
+ * h_out: h' as written by the forward, or h where there was no block.  With
+ * n = h' r and m = block r_b:
+ *   dh     = dh_out + r (weight dX - n mean(weight dX n))  (the gradient of h)
+ *   dp     = scale gate dh                                 (dh before rounding)
+ *   dblock = dp, or r_b (post_weight dp - m mean(post_weight dp m))   bf16
+ *   dweight = sum_t dX n, dgate = scale post_weight sum_t dh m,
+ *   dpost_weight = scale gate sum_t dh m                   fp32 [D]
+ * dweight NULL: no gradients of weights (frozen norms); otherwise
+ * dpost_weight and dgate are given exactly where post_weight and gate are.
+ * accumulate != 0 adds to them, each element once; T == 0 then leaves them,
+ * else sets them to 0.  dh may be dh_out.  workspace (with dweight only): at
+ * least qlora_norm_bwd_workspace_bytes, 16-byte aligned.  Deterministic (no
+ * atomics).  Errors: as the forward, and WORKSPACE.
+ */
+int qlora_norm_bwd_workspace_bytes(int64_t T, int64_t D, size_t* bytes);
+int qlora_norm_bwd(int64_t T, int64_t D, const uint16_t* dX, const void* h_out, int32_t stream_format,
+                   const uint16_t* block, const void* weight, const void* post_weight, const void* gate,
+                   int32_t weight_format, float scale, const float* stats, const void* dh_out, void* dh,
+                   uint16_t* dblock, float* dweight, float* dpost_weight, float* dgate, int32_t accumulate,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities under q = softmax(scale * z), z being the first `vocab`
+ * elements of each row of logits: format QLORA_W_F32, QLORA_W_BF16 or
+ * QLORA_W_F16, rows ld >= vocab elements apart (a head whose rows were filled
+ * up to a multiple of 64), any alignment of whole elements.  scale > 0: the
+ * reciprocal of a temperature.  T < 2^22 rows.
+ *   stats   fp32 [T][2]: M = max z and log S, S = sum exp(scale (z - M)); the
+ *           row's log-sum-exp is scale M + log S
+ *   logprob fp32 [T][n]: log q of tokens [T][n], n <= 128; a token outside
+ *           0 .. vocab - 1 (a label of -100) is none and has log probability 0
+ *   entropy fp32 [T], or NULL: -sum q log q
+ *   top_ids [T][top], top_logprob fp32 [T][top]: the `top` (<= 128, <= vocab)
+ *           largest logits of the row, largest first, ties to the lower token
+ * A logit of -inf has probability 0 (no term in the entropy).  A row of nothing
+ * else, a mask that leaves nothing, has M = log S = -inf, log probabilities
+ * -inf and entropy 0.  NaN or +inf makes its own row's log probabilities and
+ * entropy NaN; among the alternatives NaN comes last.
+ * Sums are fp32 and join in 64 bits.  Deterministic.
+ * workspace: at least qlora_token_logprob_workspace_bytes, 16-byte aligned.
+ * Errors: NULL, SHAPE, UNSUPPORTED (format, alignment, scale), WORKSPACE, HIP.
+ */
+int qlora_token_logprob_workspace_bytes(int64_t T, int64_t vocab, int32_t format, int32_t top, size_t* bytes);
+int qlora_token_logprob(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale,
+                        int32_t n, const int64_t* tokens, float* logprob, float* stats, float* entropy, int32_t top,
+                        int64_t* top_ids, float* top_logprob, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of the logits from d_logprob fp32 [T][n] and, or NULL,
+ * d_entropy fp32 [T] (which needs the forward's entropy); stats as written by
+ * the forward:
+ *   dz_j = scale ( sum over tokens that name j of d - q_j sum of all d
+ *                  - d_entropy q_j (log q_j + entropy) )
+ * Tokens that are none take no part.  dlogits has the logits' format, rows of
+ * out_cols >= vocab elements out_ld apart; columns from vocab on become 0 (so
+ * that it is the dY of a head with more rows than tokens).  dlogits may be the
+ * logits themselves, with the same row stride; otherwise the two must not
+ * overlap.  A row whose weights are all 0, and one of -inf alone, has gradient
+ * 0 whatever its logits hold.  The top alternatives carry no gradient.
+ * T * ceil(out_cols / 4096) < 2^24 is always enough (SHAPE otherwise).
+ */
+int qlora_token_logprob_bwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale,
+                            int32_t n, const int64_t* tokens, const float* stats, const float* entropy,
+                            const float* d_logprob, const float* d_entropy, void* dlogits, int64_t out_cols,
+                            int64_t out_ld, void* stream);
+
+/*
+ * Distillation from a teacher's k (1 .. 128) top tokens of each row: ids
+ * [T][k], values fp32 [T][k] (a teacher's top_ids and top_logprob, from
+ * qlora_token_logprob at this loss's temperature).  q is the student's, as
+ * above.
+ *   rest == 0: p = softmax(values) over the k tokens (values may be logits)
+ *     loss = sum_i p_i (log p_i - log q_i)
+ *   rest == 1: p = exp(values), and what is left, left = max(0, 1 - sum p), is
+ *     a bucket against the student's probability q_r outside the k tokens:
+ *     loss = sum_i p_i (log p_i - log q_i) + left (log left - log q_r)
+ * loss fp32 [T].  An id outside 0 .. vocab - 1 is no entry (a shorter list); a
+ * row without entries has loss 0 and no gradient.  A token named twice has both
+ * entries' p.  Values are finite or -inf (p = 0, no term).  p > 0 where q = 0
+ * gives +inf; where q_r = 0 the bucket is left out.
+ * stats fp32 [T][4]: M, log S, the whole of p that the gradient sees, and
+ * left / q_r (at most 1e30; 0 without a bucket).  The loss is formed in 64 bits
+ * from sums in fp32.  Deterministic.
+ * Gradient (d_loss fp32 [T]; multiply it by the square of the temperature
+ * where that is wanted):
+ *   dz_j = scale d_loss ( whole q_j - sum of the p that name j )  listed tokens
+ *        = scale d_loss ( whole - left / q_r ) q_j                the others
+ * dlogits and its columns, strides and limits as qlora_token_logprob_bwd.
+ * Rows, formats, alignment and errors as above (values, loss, stats and d_loss
+ * 4-byte, ids 8-byte aligned).
+ */
+int qlora_distill_workspace_bytes(int64_t T, int64_t vocab, int32_t format, size_t* bytes);
+int qlora_distill_fwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale, int32_t k,
+                      const int64_t* ids, const float* values, int32_t rest, float* loss, float* stats,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int qlora_distill_bwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale, int32_t k,
+                      const int64_t* ids, const float* values, int32_t rest, const float* stats, const float* d_loss,
+                      void* dlogits, int64_t out_cols, int64_t out_ld, void* stream);
+
+/*
  * AdamW update of the adapter parameters ("QLoRA技术从入门到精通" §3(3):
  * after the backward pass the optimizer updates only A and B, never the
  * quantized base weight).  The arithmetic is the published AdamW method

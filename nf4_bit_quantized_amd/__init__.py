@@ -69,6 +69,15 @@ EXPORTED = (
     "qlora_fp8_linear_bwd",
     "qlora_checkpoint_workspace_bytes",
     "qlora_linear_bwd_checkpoint",
+    "qlora_norm_fwd",
+    "qlora_norm_bwd_workspace_bytes",
+    "qlora_norm_bwd",
+    "qlora_token_logprob_workspace_bytes",
+    "qlora_token_logprob",
+    "qlora_token_logprob_bwd",
+    "qlora_distill_workspace_bytes",
+    "qlora_distill_fwd",
+    "qlora_distill_bwd",
     "qlora_adamw_step",
     "qlora_trace_enable",
     "qlora_trace_select",
@@ -151,6 +160,16 @@ def lib() -> ctypes.CDLL:
     L.qlora_checkpoint_workspace_bytes.argtypes = [dp, i64, i32, ctypes.POINTER(sz)]
     L.qlora_linear_bwd_checkpoint.argtypes = [dp, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, i32,
                                               vp, sz, vp]
+    L.qlora_norm_fwd.argtypes = [i64, i64, vp, i32, vp, vp, vp, vp, i32, f32, f32, vp, vp, vp, vp, vp, vp]
+    L.qlora_norm_bwd_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.qlora_norm_bwd.argtypes = [i64, i64, vp, vp, i32, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz,
+                                 vp]
+    L.qlora_token_logprob_workspace_bytes.argtypes = [i64, i64, i32, i32, ctypes.POINTER(sz)]
+    L.qlora_token_logprob.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.qlora_token_logprob_bwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, vp, vp, vp, vp, i64, i64, vp]
+    L.qlora_distill_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(sz)]
+    L.qlora_distill_fwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.qlora_distill_bwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
     L.qlora_adamw_step.argtypes = [ctypes.POINTER(AdamwHparams), i64, vp, vp, vp, vp, vp, vp]
     L.qlora_trace_enable.argtypes = [ctypes.c_int]
     L.qlora_trace_select.argtypes = [ctypes.c_uint32]
@@ -940,6 +959,305 @@ def qlora_checkpoint_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> i
     _check(lib().qlora_checkpoint_workspace_bytes(ctypes.byref(d), int(T), int(r), ctypes.byref(n)),
            "qlora_checkpoint_workspace_bytes")
     return n.value
+
+
+# ---------------------------------------------------------------------------
+# The two ends of the layers: residual norm, log probabilities, distillation
+# ---------------------------------------------------------------------------
+
+def _format(t, name: str, f16: bool = False) -> int:
+    import torch
+    dt = t.dtype
+    if dt == torch.bfloat16:
+        return QLORA_W_BF16
+    if dt == torch.float32:
+        return QLORA_W_F32
+    if f16 and dt == torch.float16:
+        return QLORA_W_F16
+    raise ValueError(f"{name} must be a float32{', bfloat16 or float16' if f16 else ' or bfloat16'} tensor, got {dt}")
+
+
+def _norm_args(name: str, h, block, weight, post_weight, gate):
+    """(T, D, stream format, weight format) of a residual norm."""
+    import torch
+    if h is None or h.dim() != 2 or not h.is_contiguous():
+        raise ValueError(f"{name}: the stream must be a contiguous 2-D tensor")
+    T, D = h.shape
+    if weight is None:
+        raise ValueError(f"{name}: weight is required")
+    if block is not None:
+        _check_in(block, (T, D), torch.bfloat16, "block")
+    elif post_weight is not None or gate is not None:
+        raise ValueError(f"{name}: post_weight and gate need a block")
+    for t, what in ((weight, "weight"), (post_weight, "post_weight"), (gate, "gate")):
+        if t is not None:
+            _check_in(t, (D,), weight.dtype, what)
+    return T, D, _format(h, "the stream"), _format(weight, "weight")
+
+
+def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
+                   form: str = "bf16", h_out=None, X=None, codes=None, scales=None, stats=None, stream=None):
+    """The residual norm: h' = h + scale * gate * post_weight * norm(block), x = weight * norm(h'); returns
+    (x, h', stats).  h float32 or bfloat16 [T][D]; block bf16 [T][D] or None (h' is then h itself); without
+    post_weight the block is not normalised; weight, post_weight and gate [D], float32 or bfloat16 alike.
+    form "bf16": x is bf16 [T][D]; "fp8": the pair (codes, scales) of qlora_quantize_fp8; "both": (X, codes, scales).
+    stats float32 [T][2] is for the backward.  h_out may be h."""
+    import torch
+    name = "qlora_norm_fwd"
+    T, D, fs, fw = _norm_args(name, h, block, weight, post_weight, gate)
+    if form not in ("bf16", "fp8", "both"):
+        raise ValueError(f"{name}: form must be 'bf16', 'fp8' or 'both'")
+    wide, narrow = form != "fp8", form != "bf16"
+    if (X is not None and not wide) or ((codes is not None or scales is not None) and not narrow):
+        raise ValueError(f"{name}: an output that form={form!r} does not write")
+    if block is None and h_out is not None:
+        raise ValueError(f"{name}: h_out needs a block")
+    _check_out(h_out, (T, D), h.dtype, "h_out")
+    _check_out(X, (T, D), torch.bfloat16, "X")
+    _check_out(stats, (T, 2), torch.float32, "stats")
+    if narrow:
+        shape_s = _scales_shape(T, D, 1)
+        _check_out(codes, (T, D), torch.uint8, "codes")
+        _check_out(scales, shape_s, torch.uint8, "scales")
+    device = _one_device(name, h, weight, block, post_weight, gate, h_out, X, codes, scales, stats)
+    with _LaunchOn(device, stream, name) as st:
+        if block is not None and h_out is None:
+            h_out = torch.empty_like(h)
+        if wide and X is None:
+            X = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+        if narrow and codes is None:
+            codes = torch.empty((T, D), dtype=torch.uint8, device=device)
+        if narrow and scales is None:
+            scales = torch.empty(shape_s, dtype=torch.uint8, device=device)
+        if stats is None:
+            stats = torch.empty((T, 2), dtype=torch.float32, device=device)
+        _check(lib().qlora_norm_fwd(T, D, _ptr(h), fs, _ptr(block), _ptr(weight), _ptr(post_weight), _ptr(gate), fw,
+                                    float(scale), float(eps), _ptr(h_out), _ptr(X), _ptr(codes), _ptr(scales),
+                                    _ptr(stats), st), name)
+    x = X if form == "bf16" else (codes, scales) if form == "fp8" else (X, codes, scales)
+    return x, h if block is None else h_out, stats
+
+
+def qlora_norm_bwd_workspace_bytes(T: int, D: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_norm_bwd_workspace_bytes(int(T), int(D), ctypes.byref(n)), "qlora_norm_bwd_workspace_bytes")
+    return n.value
+
+
+def qlora_norm_bwd(dX, h_out, weight, stats, block=None, post_weight=None, gate=None, scale: float = 1.0, dh_out=None,
+                   dh=None, dblock=None, dweight=None, dpost_weight=None, dgate=None, want_weights: bool = True,
+                   workspace=None, stream=None, accumulate: bool = False):
+    """Backward of qlora_norm_fwd from dX bf16 [T][D] and dh_out (the gradient of h' from behind, or None); returns
+    (dh, dblock, dweight, dpost_weight, dgate), None for what there is not.  want_weights=False: frozen weights.
+    accumulate=True adds to the given dweight, dpost_weight and dgate (float32 [D]).  dh may be dh_out."""
+    import torch
+    name = "qlora_norm_bwd"
+    T, D, fs, fw = _norm_args(name, h_out, block, weight, post_weight, gate)
+    _check_in(dX, (T, D), torch.bfloat16, "dX")
+    _check_in(stats, (T, 2), torch.float32, "stats")
+    _check_out(dh_out, (T, D), h_out.dtype, "dh_out")
+    _check_out(dh, (T, D), h_out.dtype, "dh")
+    if block is None and dblock is not None:
+        raise ValueError(f"{name}: dblock needs a block")
+    _check_out(dblock, (T, D), torch.bfloat16, "dblock")
+    grads = ((dweight, weight, "dweight"), (dpost_weight, post_weight, "dpost_weight"), (dgate, gate, "dgate"))
+    for g, w, what in grads:
+        if g is not None and (w is None or not want_weights):
+            raise ValueError(f"{name}: {what} is not written by this call")
+        if g is None and w is not None and want_weights and accumulate:
+            raise ValueError(f"{name}: accumulate=True needs the {what} to add to")
+        _check_out(g, (D,), torch.float32, what)
+    device = _one_device(name, dX, h_out, weight, stats, block, post_weight, gate, dh_out, dh, dblock, dweight,
+                         dpost_weight, dgate, workspace)
+    with _LaunchOn(device, stream, name) as st:
+        if dh is None:
+            dh = torch.empty_like(h_out)
+        if block is not None and dblock is None:
+            dblock = torch.empty_like(block)
+        nbytes = 0
+        if want_weights:
+            dweight, dpost_weight, dgate = (
+                torch.empty(D, dtype=torch.float32, device=device) if g is None and w is not None else g
+                for g, w, _ in grads)
+            nbytes = qlora_norm_bwd_workspace_bytes(T, D)
+        ws = _workspace(nbytes, device, workspace)
+        _check(lib().qlora_norm_bwd(T, D, _ptr(dX), _ptr(h_out), fs, _ptr(block), _ptr(weight), _ptr(post_weight),
+                                    _ptr(gate), fw, float(scale), _ptr(stats), _ptr(dh_out), _ptr(dh), _ptr(dblock),
+                                    _ptr(dweight), _ptr(dpost_weight), _ptr(dgate), 1 if accumulate else 0, _ptr(ws),
+                                    nbytes, st), name)
+    return dh, dblock, dweight, dpost_weight, dgate
+
+
+def _logits_rows(name: str, logits, vocab):
+    """(T, vocab, format, row stride) of logits [T][columns >= vocab], columns contiguous."""
+    if logits is None or logits.dim() != 2:
+        raise ValueError(f"{name}: logits must be a 2-D tensor")
+    T, cols = logits.shape
+    vocab = cols if vocab is None else int(vocab)
+    if not 0 < vocab <= cols:
+        raise ValueError(f"{name}: vocab must be in 1 .. {cols}, the logits' columns")
+    ld = logits.stride(0) if T > 1 else cols
+    if (logits.stride(1) != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name}: the logits' rows must be contiguous and must not overlap")
+    return T, vocab, _format(logits, "logits", f16=True), ld
+
+
+def _entries(name: str, ids, T: int, what: str):
+    """The number of ids per row: [T] (one) or [T][n], int64, contiguous."""
+    import torch
+    if ids.dtype != torch.int64 or ids.dim() not in (1, 2) or ids.shape[0] != T or not ids.is_contiguous():
+        raise ValueError(f"{name}: {what} must be a contiguous int64 tensor of shape ({T},) or ({T}, n)")
+    return 1 if ids.dim() == 1 else ids.shape[1]
+
+
+@functools.lru_cache(maxsize=256)      # the sizes decide it
+def qlora_token_logprob_workspace_bytes(T: int, vocab: int, format: int, top: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_token_logprob_workspace_bytes(T, vocab, format, top, ctypes.byref(n)),
+           "qlora_token_logprob_workspace_bytes")
+    return n.value
+
+
+def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy: bool = False,
+                        vocab: Optional[int] = None, logprob=None, stats=None, entropy=None, top_ids=None,
+                        top_logprob=None, workspace=None, stream=None):
+    """Log probabilities under softmax(scale * logits[:, :vocab]): returns (logprob, stats, entropy, top_ids,
+    top_logprob), None for what was not asked.  logits float32, bfloat16 or float16 [T][columns], rows at any stride;
+    tokens int64 [T] or [T][n], an entry outside 0 .. vocab - 1 (-100) has log probability 0; logprob float32 of
+    their shape.  stats float32 [T][2] (M, log S) is for the backward; scale * M + log S is the log-sum-exp.
+    top_ids int64, top_logprob float32 [T][top]: the largest, ties to the lower token."""
+    import torch
+    name = "qlora_token_logprob"
+    T, vocab, fmt, ld = _logits_rows(name, logits, vocab)
+    n = 0 if tokens is None else _entries(name, tokens, T, "tokens")
+    top = int(top)
+    if tokens is None and logprob is not None:
+        raise ValueError(f"{name}: logprob needs tokens")
+    if tokens is not None:
+        _check_out(logprob, tokens.shape, torch.float32, "logprob")
+    _check_out(stats, (T, 2), torch.float32, "stats")
+    _check_out(entropy, (T,), torch.float32, "entropy")
+    _check_out(top_ids, (T, top), torch.int64, "top_ids")
+    _check_out(top_logprob, (T, top), torch.float32, "top_logprob")
+    device = _one_device(name, logits, tokens, logprob, stats, entropy, top_ids, top_logprob, workspace)
+    nbytes = qlora_token_logprob_workspace_bytes(T, vocab, fmt, top)
+    with _LaunchOn(device, stream, name) as st:
+        if tokens is not None and logprob is None:
+            logprob = torch.empty(tokens.shape, dtype=torch.float32, device=device)
+        if stats is None:
+            stats = torch.empty((T, 2), dtype=torch.float32, device=device)
+        if want_entropy and entropy is None:
+            entropy = torch.empty((T,), dtype=torch.float32, device=device)
+        if top > 0 and top_ids is None:
+            top_ids = torch.empty((T, top), dtype=torch.int64, device=device)
+        if top > 0 and top_logprob is None:
+            top_logprob = torch.empty((T, top), dtype=torch.float32, device=device)
+        ws = _workspace(nbytes, device, workspace)
+        _check(lib().qlora_token_logprob(T, vocab, _ptr(logits), fmt, ld, float(scale), n, _ptr(tokens), _ptr(logprob),
+                                         _ptr(stats), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprob), _ptr(ws),
+                                         nbytes, st), name)
+    return logprob, stats, entropy, top_ids, top_logprob
+
+
+def _gradient_rows(name: str, logits, dlogits):
+    """The row stride of given gradients: the logits' shape and dtype, columns contiguous."""
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        raise ValueError(f"{name}: dlogits must have the logits' shape and dtype")
+    T, cols = dlogits.shape
+    ld = dlogits.stride(0) if T > 1 else cols
+    if (dlogits.stride(1) != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name}: the rows of dlogits must be contiguous and must not overlap")
+    return ld
+
+
+def qlora_token_logprob_bwd(logits, tokens, stats, d_logprob, scale: float = 1.0, entropy=None, d_entropy=None,
+                            vocab: Optional[int] = None, dlogits=None, stream=None):
+    """The gradient of the logits, in their shape and dtype (zeros from column vocab on), from d_logprob float32 (the
+    tokens' shape) and d_entropy float32 [T] (with the forward's entropy); stats as the forward wrote them.  tokens
+    and d_logprob may be None for the entropy's gradient alone.  dlogits may be the logits."""
+    import torch
+    name = "qlora_token_logprob_bwd"
+    T, vocab, fmt, ld = _logits_rows(name, logits, vocab)
+    n = 0 if tokens is None else _entries(name, tokens, T, "tokens")
+    if tokens is not None:
+        _check_in(d_logprob, tokens.shape, torch.float32, "d_logprob")
+    elif d_logprob is not None or d_entropy is None:
+        raise ValueError(f"{name}: tokens with d_logprob, or d_entropy, are required")
+    _check_in(stats, (T, 2), torch.float32, "stats")
+    if d_entropy is not None:
+        _check_in(d_entropy, (T,), torch.float32, "d_entropy")
+        _check_in(entropy, (T,), torch.float32, "entropy")
+    device = _one_device(name, logits, tokens, stats, d_logprob, entropy, d_entropy, dlogits)
+    with _LaunchOn(device, stream, name) as st:
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+        _check(lib().qlora_token_logprob_bwd(T, vocab, _ptr(logits), fmt, ld, float(scale), n, _ptr(tokens),
+                                             _ptr(stats), _ptr(entropy), _ptr(d_logprob), _ptr(d_entropy),
+                                             _ptr(dlogits), logits.shape[1], _gradient_rows(name, logits, dlogits),
+                                             st), name)
+    return dlogits
+
+
+@functools.lru_cache(maxsize=256)      # the sizes decide it
+def qlora_distill_workspace_bytes(T: int, vocab: int, format: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_distill_workspace_bytes(T, vocab, format, ctypes.byref(n)), "qlora_distill_workspace_bytes")
+    return n.value
+
+
+def _teacher(name: str, ids, values, T: int) -> int:
+    """k of a teacher's ids int64 and values float32, both [T][k]."""
+    import torch
+    if ids is None or ids.dim() != 2:
+        raise ValueError(f"{name}: ids must be a 2-D tensor")
+    k = _entries(name, ids, T, "ids")
+    _check_in(values, (T, k), torch.float32, "values")
+    return k
+
+
+def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = False, vocab: Optional[int] = None,
+                      loss=None, stats=None, workspace=None, stream=None):
+    """The distillation loss of each row, sum p (log p - log q), q = softmax(scale * logits[:, :vocab]): returns
+    (loss float32 [T], stats float32 [T][4]).  p from the teacher's ids int64 [T][k] and values float32 [T][k] (its
+    top_ids and top_logprob): softmax(values), or with rest=True exp(values) and what is left to 1 as one more
+    bucket.  An id outside 0 .. vocab - 1 is no entry."""
+    import torch
+    name = "qlora_distill_fwd"
+    T, vocab, fmt, ld = _logits_rows(name, logits, vocab)
+    k = _teacher(name, ids, values, T)
+    _check_out(loss, (T,), torch.float32, "loss")
+    _check_out(stats, (T, 4), torch.float32, "stats")
+    device = _one_device(name, logits, ids, values, loss, stats, workspace)
+    nbytes = qlora_distill_workspace_bytes(T, vocab, fmt)
+    with _LaunchOn(device, stream, name) as st:
+        if loss is None:
+            loss = torch.empty((T,), dtype=torch.float32, device=device)
+        if stats is None:
+            stats = torch.empty((T, 4), dtype=torch.float32, device=device)
+        ws = _workspace(nbytes, device, workspace)
+        _check(lib().qlora_distill_fwd(T, vocab, _ptr(logits), fmt, ld, float(scale), k, _ptr(ids), _ptr(values),
+                                       1 if rest else 0, _ptr(loss), _ptr(stats), _ptr(ws), nbytes, st), name)
+    return loss, stats
+
+
+def qlora_distill_bwd(logits, ids, values, stats, d_loss, scale: float = 1.0, rest: bool = False,
+                      vocab: Optional[int] = None, dlogits=None, stream=None):
+    """The gradient of the logits, in their shape and dtype (zeros from column vocab on), from d_loss float32 [T];
+    stats as qlora_distill_fwd wrote them.  dlogits may be the logits."""
+    import torch
+    name = "qlora_distill_bwd"
+    T, vocab, fmt, ld = _logits_rows(name, logits, vocab)
+    k = _teacher(name, ids, values, T)
+    _check_in(stats, (T, 4), torch.float32, "stats")
+    _check_in(d_loss, (T,), torch.float32, "d_loss")
+    device = _one_device(name, logits, ids, values, stats, d_loss, dlogits)
+    with _LaunchOn(device, stream, name) as st:
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+        _check(lib().qlora_distill_bwd(T, vocab, _ptr(logits), fmt, ld, float(scale), k, _ptr(ids), _ptr(values),
+                                       1 if rest else 0, _ptr(stats), _ptr(d_loss), _ptr(dlogits), logits.shape[1],
+                                       _gradient_rows(name, logits, dlogits), st), name)
+    return dlogits
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,382 @@
+// Log probabilities of given tokens, with the entropy and the most likely
+// tokens of the row, and the distillation loss against a teacher's top logits.
+//
+// With q = softmax(scale * z) over a row of logits z, M = max z:
+//   S = sum exp(scale (z - M)),  log q_j = scale (z_j - M) - log S
+//   H = log S - sum exp(scale (z - M)) scale (z - M) / S
+// One pass over the row: each thread keeps its largest element and, relative to
+// a whole number R near its largest scale * z * log2(e), the sum of 2^(y - R)
+// and for H of 2^(y - R) (y - R), y = c z, c = fl32(scale * log2(e)).  R is
+// whole, so changing from one R to another is exact; y - R is one FMA, rounded
+// once; and the workgroup's result is brought from R to c M in 64 bits with the
+// same c, so nothing that is common to a row is rounded in 32 bits but the
+// terms themselves and their sums.
+//
+// A logit of -inf has probability 0.  A row of nothing else has M = -inf,
+// log S = -inf: log probabilities -inf, entropy 0.  NaN or +inf in a row makes
+// the row's results NaN.  Where |c M| >= 2^24, R is no longer exact enough and
+// the row is read a second time with z - M formed first: so masks of the type's
+// lowest value, rows of nothing else among them, give their probabilities too.
+#include <type_traits>
+
+#include "logits.hpp"
+#include "logits_top.hpp"
+#include "trace.hpp"
+#include "wave.hpp"
+
+namespace qlora {
+namespace {
+
+using namespace logits;
+
+constexpr float kFar = 1.329227995784916e36f;  // 2^120
+
+struct Sums {
+  float m = -kMost, R = -kFar, s = 0.0f, t = 0.0f;
+};
+
+template <int N, bool ENT>
+__device__ __forceinline__ void add(Sums& a, const float (&f)[N], float c) {
+  float g = f[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) g = fmaxf(g, f[e]);
+  a.m = fmaxf(a.m, g);
+  const float y = g * c;
+  if (y > a.R + 32.0f) {  // sums up to 2^32 times the count stay far inside the range
+    const float R = fminf(rintf(y), kFar), d = a.R - R, k = __builtin_amdgcn_exp2f(d);
+    if constexpr (ENT) a.t = k > 0.0f ? (a.t + a.s * d) * k : 0.0f;
+    a.s *= k;
+    a.R = R;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float d = __builtin_fmaf(f[e], c, -a.R), x = __builtin_amdgcn_exp2f(d);
+    a.s += x;
+    if constexpr (ENT) a.t = __builtin_fmaf(x, fmaxf(d, -kFar), a.t);  // 0 * -inf stays 0
+  }
+}
+
+// The tokens of a teacher's list: bit b of byte p - first stands for element b
+// of piece p, in a window of kWindow pieces.
+constexpr int kWindow = 8192;
+
+template <int F, bool ENT, bool MASK, int THREADS>
+__device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first) {
+  constexpr int E = kPer<F>, U = 4;
+  int p = p0 + (int)threadIdx.x;
+  for (; p + (U - 1) * THREADS < p1; p += U * THREADS) {
+    u32x4_t w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = row.load(p + u * THREADS);
+    float f[U * E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      unpack<F>(w[u], f + u * E);
+      if constexpr (MASK) {
+        const uint32_t b = mask[p + u * THREADS - first];
+        if (b)
+          for (int e = 0; e < E; ++e) f[u * E + e] = (b >> e) & 1u ? kNone : f[u * E + e];
+      }
+    }
+    add<U * E, ENT>(a, f, c);
+  }
+  for (; p < p1; p += THREADS) {
+    float f[E];
+    unpack<F>(row.load(p), f);
+    if constexpr (MASK) {
+      const uint32_t b = mask[p - first];
+      if (b)
+        for (int e = 0; e < E; ++e) f[e] = (b >> e) & 1u ? kNone : f[e];
+    }
+    add<E, ENT>(a, f, c);
+  }
+}
+
+struct Reduced {
+  float m[16];
+  double s[16], t[16];
+};
+
+// What a row (or a part of one) comes to: M, S and T = sum e log2(e) with
+// e = 2^(c (z - M)).
+struct Stats {
+  float M;
+  double S, T;
+};
+
+template <int THREADS>
+__device__ __forceinline__ float block_max(float m, Reduced& sh) {
+  m = wave::largest(m);
+  if ((threadIdx.x & 63) == 0) sh.m[threadIdx.x >> 6] = m;
+  __syncthreads();
+  float v = sh.m[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) v = fmaxf(v, sh.m[w]);
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double& S, double& T) {
+  const double ds = wave::sum((double)s), dt = wave::sum((double)t);
+  if ((threadIdx.x & 63) == 0) {
+    sh.s[threadIdx.x >> 6] = ds;
+    sh.t[threadIdx.x >> 6] = dt;
+  }
+  __syncthreads();
+  S = T = 0.0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    S += sh.s[w];
+    T += sh.t[w];
+  }
+}
+
+// The statistics of pieces p0 .. p1 - 1 and, with `edges`, of the elements
+// outside the full pieces; every thread gets them.  With MASK the k elements of
+// ids are left out.
+template <int F, bool ENT, bool MASK, int THREADS>
+__device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
+                            uint32_t* mask, Reduced& sh) {
+  constexpr int E = kPer<F>;
+  const auto listed = [&](int64_t i) {
+    bool hit = false;
+    if constexpr (MASK)
+      for (int j = 0; j < k; ++j) hit |= ids[j] == i;
+    return hit;
+  };
+  const auto pass = [&](const auto& body) {
+    for (int q0 = p0; q0 < p1; q0 += MASK ? kWindow : p1 - p0) {
+      const int q1 = MASK && q0 + kWindow < p1 ? q0 + kWindow : p1;
+      if constexpr (MASK) {
+        __syncthreads();
+        for (int w = (int)threadIdx.x; w < kWindow / 4; w += THREADS) mask[w] = 0u;
+        __syncthreads();
+        if ((int)threadIdx.x < k) {
+          const int64_t id = ids[threadIdx.x], at = id + row.head;
+          const int64_t p = at / E;
+          if (id >= 0 && id < row.vocab && p >= q0 && p < q1)
+            atomicOr(&mask[(p - q0) >> 2], 1u << (8 * ((p - q0) & 3) + (int)(at - p * E)));
+        }
+        __syncthreads();
+      }
+      body(q0, q1);
+    }
+  };
+  Sums a;
+  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
+  const int mine = edges && (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
+  const float z_edge = mine >= 0 && !listed(mine) ? row.at(mine) : kNone;
+  {
+    const float f[1] = {z_edge};
+    if (mine >= 0) add<1, ENT>(a, f, c);
+  }
+  Stats r;
+  r.M = block_max<THREADS>(a.m, sh);
+  const float y = r.M * c;
+  if (!(fabsf(y) < 16777216.0f)) {
+    float s = 0.0f, t = 0.0f;
+    const auto one = [&](float z) {
+      const float d = (z - r.M) * c, x = __builtin_amdgcn_exp2f(d);
+      s += x;
+      if constexpr (ENT) t = __builtin_fmaf(x, fmaxf(d, -kFar), t);
+    };
+    pass([&](int q0, int q1) {
+      for (int p = q0 + (int)threadIdx.x; p < q1; p += THREADS) {
+        float f[E];
+        unpack<F>(row.load(p), f);
+        uint32_t b = 0;
+        if constexpr (MASK) b = reinterpret_cast<const uint8_t*>(mask)[p - q0];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!((b >> e) & 1u)) one(f[e]);
+      }
+    });
+    if (mine >= 0) one(z_edge);
+    block_sum<THREADS>(s, t, sh, r.S, r.T);
+  } else {
+    const float R = rintf(y), d = a.R - R, k2 = __builtin_amdgcn_exp2f(d);
+    block_sum<THREADS>(a.s * k2, ENT && k2 > 0.0f ? (a.t + a.s * d) * k2 : 0.0f, sh, r.S, r.T);
+    const double off = (double)R - (double)c * (double)r.M, f = exp2(off);
+    if constexpr (ENT) r.T = (r.T + r.S * off) * f;
+    r.S *= f;
+  }
+  if (r.S == 0.0) r.M = kNone;
+  return r;
+}
+
+// log q of a logit
+__device__ __forceinline__ float log_q(float z, float M, double scale, double log_s) {
+  if (M == kNone) return kNone;
+  return (float)(scale * ((double)z - (double)M) - log_s);
+}
+
+template <int F, bool ENT, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
+  __shared__ Reduced red;
+  __shared__ TopShared top;
+  const int64_t t = blockIdx.x;
+  const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
+  const Stats r = statistics<F, ENT, false, THREADS>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red);
+  const double log_s = log(r.S), scale = (double)P.in.scale;
+  if (threadIdx.x == 0) {
+    P.stats[2 * t] = r.M;
+    P.stats[2 * t + 1] = (float)log_s;
+    if constexpr (ENT) P.entropy[t] = r.S == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (r.T / r.S));
+  }
+  for (int i = (int)threadIdx.x; i < P.n; i += THREADS) {
+    const int64_t id = P.tokens[t * P.n + i];
+    P.logprob[t * P.n + i] = id >= 0 && id < P.in.vocab ? log_q(row.at(id), r.M, scale, log_s) : 0.0f;
+  }
+  if (P.top > 0) {
+    top_bisect<F, THREADS>(row, row.full0, row.full1, true, P.top, 0, ~(uint64_t)0, top);
+    top_ranked<THREADS>(top, P.top, [&](int rank, uint64_t key) {
+      P.top_ids[t * P.top + rank] = top_index(key);
+      P.top_logprob[t * P.top + rank] = log_q(top_value(key), r.M, scale, log_s);
+    });
+  }
+}
+
+// The loss of a row from the statistics of its elements (with REST, of those
+// that are not in the teacher's list), by one wave with two entries to a lane.
+// Everything is in 64 bits: the loss is a small difference of large terms.
+//   rest == 0: p = softmax(values);  loss = sum p (log p - log q)
+//   rest == 1: p = exp(values), left = max(0, 1 - sum p), and with q_r the
+//     probability outside the list  loss += left (log left - log q_r)
+// stats: M, log S, and what the gradient scale * (whole q - p) takes: `whole`
+// for the listed tokens, whole - ratio for the others (ratio = left / q_r).
+// Entries outside 0 .. vocab - 1 are left out; with none left, whole = 0.  Where
+// q_r = 0 the bucket is left out.
+template <int F, bool REST>
+__device__ void distill_finish(const DistillParams& P, int64_t t, const Row<F>& row, Stats r) {
+  const int lane = (int)threadIdx.x;
+  const double scale = (double)P.in.scale;
+  int64_t id[2];
+  bool in[2];
+  double v[2];
+  float z[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 64 * h;
+    id[h] = i < P.k ? P.ids[t * P.k + i] : -1;
+    in[h] = id[h] >= 0 && id[h] < P.in.vocab;
+    v[h] = in[h] ? (double)P.values[t * P.k + i] : -__builtin_inf();
+    z[h] = in[h] ? row.at(id[h]) : kNone;
+  }
+  const bool any = __ballot(in[0] || in[1]) != 0;
+  double known = 0.0, log_known = 0.0;
+  if constexpr (!REST) {
+    const double most = (double)wave::largest(fmaxf((float)v[0], (float)v[1]));
+    if (most > -__builtin_inf()) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] -= most;
+      known = wave::sum(exp(v[0]) + exp(v[1]));
+      log_known = log(known);
+    }
+  } else {
+    known = wave::sum(exp(v[0]) + exp(v[1]));
+    // the listed elements join the sum, each token once
+    bool first[2] = {in[0], in[1]};
+    for (int j = 0; j < P.k; ++j) {
+      const int64_t other = P.ids[t * P.k + j];
+      first[0] = first[0] && !(j < lane && other == id[0]);
+      first[1] = first[1] && !(j < lane + 64 && other == id[1]);
+    }
+    const float most = fmaxf(r.M, wave::largest(fmaxf(z[0], z[1])));
+    if (most > kNone) {
+      double s = 0.0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (first[h]) s += exp(scale * ((double)z[h] - (double)most));
+      s = wave::sum(s);
+      r.S *= r.S == 0.0 ? 0.0 : exp(scale * ((double)r.M - (double)most));
+      r.M = most;
+      r.T = r.S;  // the sum outside the list
+      r.S += s;
+    } else {
+      r.T = r.S;
+    }
+  }
+  const double log_s = log(r.S);
+  double loss = 0.0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const double lp = v[h] - log_known, p = exp(lp);
+    if (p > 0.0) loss += p * (lp - (scale * ((double)z[h] - (double)r.M) - log_s));
+  }
+  loss = wave::sum(loss);
+  double whole = any && known > 0.0 ? 1.0 : 0.0, ratio = 0.0;
+  if constexpr (REST) {
+    whole = known;
+    const double left = 1.0 - known;
+    if (any && left > 0.0 && r.T > 0.0) {
+      const double q_r = r.T / r.S;
+      loss += left * (log(left) - log(q_r));
+      ratio = left / q_r;
+      whole = 1.0;
+    }
+  }
+  if (r.S == 0.0) loss = whole > 0.0 ? __builtin_inf() : 0.0;
+  if (r.S != r.S && any) loss = r.S;
+  if (lane == 0) {
+    P.loss[t] = (float)loss;
+    P.stats[4 * t] = r.M;
+    P.stats[4 * t + 1] = (float)log_s;
+    P.stats[4 * t + 2] = (float)whole;
+    P.stats[4 * t + 3] = (float)fmin(ratio, 1e30);
+  }
+}
+
+template <int F, bool REST, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_distill(DistillParams P, float c) {
+  __shared__ Reduced red;
+  __shared__ uint32_t mask[REST ? kWindow / 4 : 1];
+  const int64_t t = blockIdx.x;
+  const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
+  const Stats r = statistics<F, false, REST, THREADS>(row, row.full0, row.full1, true, c, P.ids + t * P.k, P.k, mask, red);
+  if (threadIdx.x < 64) distill_finish<F, REST>(P, t, row, r);
+}
+
+float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
+constexpr int kThreads = 512;
+
+}  // namespace
+
+size_t score_part_bytes(int64_t, int64_t, int, int) { return 0; }
+size_t distill_part_bytes(int64_t, int64_t, int) { return 0; }
+
+hipError_t launch_score(const ScoreParams& P, hipStream_t stream) {
+  if (P.in.T == 0) return hipSuccess;
+  KernelEvents ev(KID_LOGPROB);
+  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
+  const float c = log2_scale(P.in.scale);
+  const dim3 grid((unsigned)P.in.T), block(kThreads);
+  const auto go = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (P.entropy) hipExtLaunchKernelGGL((k_score<F, true, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
+    else hipExtLaunchKernelGGL((k_score<F, false, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
+  };
+  if (P.in.format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
+  else if (P.in.format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());
+  else go(std::integral_constant<int, kWeightF16>());
+  return hipGetLastError();
+}
+
+hipError_t launch_distill(const DistillParams& P, hipStream_t stream) {
+  if (P.in.T == 0) return hipSuccess;
+  KernelEvents ev(KID_DISTILL);
+  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
+  const float c = log2_scale(P.in.scale);
+  const dim3 grid((unsigned)P.in.T), block(kThreads);
+  const auto go = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (P.rest) hipExtLaunchKernelGGL((k_distill<F, true, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
+    else hipExtLaunchKernelGGL((k_distill<F, false, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
+  };
+  if (P.in.format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
+  else if (P.in.format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());
+  else go(std::integral_constant<int, kWeightF16>());
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -11,7 +11,8 @@ namespace {
 const char* const kNames[KID_COUNT] = {
     "nf4_quantize", "fwd_gemm", "dx_gemm", "lora_down_gemm", "lora_g_gemm", "lora_grad_gemm",
     "lora_db_gemm", "decode", "reduce", "fill_zero", "export", "adamw", "dropout", "decode_sum",
-    "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_down", "fp8_grad"};
+    "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_down", "fp8_grad",
+    "norm", "norm_bwd", "norm_sum", "logprob", "distill", "logits_grad"};
 
 struct Pending {
   int kid;

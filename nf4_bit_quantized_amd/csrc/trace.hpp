@@ -27,6 +27,12 @@ enum KernelId : int {
   KID_FP8_GEMM,
   KID_FP8_DOWN,
   KID_FP8_GRAD,
+  KID_NORM,
+  KID_NORM_BWD,
+  KID_NORM_SUM,
+  KID_LOGPROB,
+  KID_DISTILL,
+  KID_LOGITS_GRAD,
   KID_COUNT
 };
 

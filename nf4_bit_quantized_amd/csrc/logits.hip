@@ -117,7 +117,7 @@ __device__ __forceinline__ float block_max(float m, Reduced& sh) {
 
 template <int THREADS>
 __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double& S, double& T) {
-  const double ds = wave::sum((double)s), dt = wave::sum((double)t);
+  const double ds = (double)wave::sum(s), dt = (double)wave::sum(t);
   if ((threadIdx.x & 63) == 0) {
     sh.s[threadIdx.x >> 6] = ds;
     sh.t[threadIdx.x >> 6] = dt;
@@ -136,7 +136,7 @@ __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double&
 // ids are left out.
 template <int F, bool ENT, bool MASK, int THREADS>
 __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
-                            uint32_t* mask, Reduced& sh) {
+                            uint32_t* mask, Reduced& sh, float* most = nullptr) {
   constexpr int E = kPer<F>;
   const auto listed = [&](int64_t i) {
     bool hit = false;
@@ -170,6 +170,7 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
     const float f[1] = {z_edge};
     if (mine >= 0) add<1, ENT>(a, f, c);
   }
+  if (most) *most = a.m;
   Stats r;
   r.M = block_max<THREADS>(a.m, sh);
   const float y = r.M * c;
@@ -213,10 +214,11 @@ __device__ __forceinline__ float log_q(float z, float M, double scale, double lo
 template <int F, bool ENT, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   __shared__ Reduced red;
-  __shared__ TopShared top;
+  __shared__ TopShared sh_top;
   const int64_t t = blockIdx.x;
   const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
-  const Stats r = statistics<F, ENT, false, THREADS>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red);
+  float most;
+  const Stats r = statistics<F, ENT, false, THREADS>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
   const double log_s = log(r.S), scale = (double)P.in.scale;
   if (threadIdx.x == 0) {
     P.stats[2 * t] = r.M;
@@ -228,8 +230,8 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
     P.logprob[t * P.n + i] = id >= 0 && id < P.in.vocab ? log_q(row.at(id), r.M, scale, log_s) : 0.0f;
   }
   if (P.top > 0) {
-    top_bisect<F, THREADS>(row, row.full0, row.full1, true, P.top, 0, ~(uint64_t)0, top);
-    top_ranked<THREADS>(top, P.top, [&](int rank, uint64_t key) {
+    top_candidates<F, THREADS>(row, row.full0, row.full1, true, P.top, most, sh_top);
+    top_ranked<THREADS>(sh_top.key, sh_top.count, P.top, [&](int rank, uint64_t key) {
       P.top_ids[t * P.top + rank] = top_index(key);
       P.top_logprob[t * P.top + rank] = log_q(top_value(key), r.M, scale, log_s);
     });

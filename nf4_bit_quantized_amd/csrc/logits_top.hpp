@@ -20,8 +20,29 @@ __device__ __forceinline__ float top_value(uint64_t key) { return from_ordered((
 
 struct TopShared {
   uint64_t key[kCandidates];
-  int count;
+  uint64_t near[kCandidates];  // top_narrow's
+  uint32_t most[256];          // keys of the groups of threads
+  uint16_t who[1024];          // threads that hold candidates
+  int count, holders;
+  uint32_t low;
 };
+
+// The largest t with at least K of n keys (at most 64 * N) >= t, or one that
+// lets exactly K pass; 0 if there are fewer than K.  By one wave, bit by bit
+// from the top, `bits` of them: the bits below stay 0, and more may pass.
+template <int N>
+__device__ __forceinline__ uint32_t top_limit(const uint32_t (&key)[N], int K, int bits) {
+  uint32_t t = 0;
+  for (int b = 31; b >= 32 - bits; --b) {
+    const uint32_t next = t | (1u << b);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) n += __popcll(__ballot(key[j] >= next));
+    if (n >= K) t = next;
+    if (n == K) break;
+  }
+  return t;
+}
 
 // Calls at(value, index) for the elements of pieces p0 .. p1 - 1 and, with
 // `edges`, for those outside the full pieces.
@@ -77,15 +98,99 @@ __device__ void top_bisect(const Row<F>& row, int p0, int p1, bool edges, int K,
   __syncthreads();
 }
 
-// Calls out(rank, key) for the K largest of sh's candidates, rank 0 the
-// largest.  They arrived in any order; their keys alone decide.
-template <int THREADS, class Out>
-__device__ __forceinline__ void top_ranked(const TopShared& sh, int K, const Out& out) {
-  const int n = sh.count < kCandidates ? sh.count : kCandidates;
+// The same with a pass over few pieces: `most` is the largest element of the
+// pieces p0 + threadIdx.x + j * THREADS (and of an edge) that this thread has
+// read, never above it and at least -kMost.  Of 256 groups of threads, K have
+// their largest element at or above the limit; so K elements are, and whatever
+// is lies with a thread whose `most` is: those threads' pieces alone are read
+// again.  Of 128256 logits by 512 threads, about K of 512 in the mean, all at
+// once.  Rows of many like elements overflow the candidates and are bisected.
+template <int F, int THREADS>
+__device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, int K, float most, TopShared& sh) {
+  constexpr int G = THREADS / 256;
+  const uint32_t mine = most > -kMost ? ordered(most) : 0u;
+  uint32_t group = mine;
+  if constexpr (G >= 2) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)group, 0xB1, 0xF, 0xF, false);  // lane ^ 1
+    group = o > group ? o : group;
+  }
+  if constexpr (G >= 4) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)group, 0x4E, 0xF, 0xF, false);  // lane ^ 2
+    group = o > group ? o : group;
+  }
+  if ((int)threadIdx.x % G == 0) sh.most[threadIdx.x / G] = group;
+  if (threadIdx.x == 0) sh.count = sh.holders = 0;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    uint32_t key[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key[j] = sh.most[64 * j + threadIdx.x];
+    // the type of the logits decides sixteen bits of a key; for fp32 it is a limit all the same
+    const uint32_t low = top_limit<4>(key, K, 16);
+    if (threadIdx.x == 0) sh.low = low;
+  }
+  __syncthreads();
+  const uint32_t low = sh.low;
+  if (mine >= low) sh.who[atomicAdd(&sh.holders, 1)] = (uint16_t)threadIdx.x;
+  __syncthreads();
+  const auto offer = [&](float v, int64_t i) {
+    const uint32_t k = ordered(v);
+    if (k < low) return;
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCandidates) sh.key[at] = ((uint64_t)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+  };
+  const int holders = sh.holders, each = (p1 - p0 + THREADS - 1) / THREADS;
+  for (int x = (int)threadIdx.x; x < holders * each; x += THREADS) {
+    const int j = x / holders, p = p0 + (int)sh.who[x - j * holders] + j * THREADS;
+    if (p >= p1) continue;
+    float f[kPer<F>];
+    unpack<F>(row.load(p), f);
+    const int64_t i0 = (int64_t)p * kPer<F> - row.head;
+#pragma unroll
+    for (int e = 0; e < kPer<F>; ++e) offer(f[e], i0 + e);
+  }
+  if (edges && (int)threadIdx.x < row.edges()) {
+    const int i = row.edge((int)threadIdx.x);
+    offer(row.at(i), (int64_t)i);
+  }
+  __syncthreads();
+  if (sh.count > kCandidates) top_bisect<F, THREADS>(row, p0, p1, edges, K, (uint64_t)low << 32, ~(uint64_t)0, sh);
+}
+
+// Leaves of sh's candidates those that reach the K-th largest's first 32 bits.
+template <int THREADS>
+__device__ void top_narrow(int K, TopShared& sh) {
+  const int n = sh.count;
+  if (threadIdx.x < 64) {
+    uint32_t key[kCandidates / 64];
+#pragma unroll
+    for (int j = 0; j < kCandidates / 64; ++j) {
+      const int i = 64 * j + (int)threadIdx.x;
+      key[j] = i < n ? (uint32_t)(sh.key[i] >> 32) : 0u;
+    }
+    const uint32_t low = top_limit<kCandidates / 64>(key, K, 32);
+    if (threadIdx.x == 0) {
+      sh.low = low;
+      sh.holders = 0;
+    }
+  }
+  __syncthreads();
+  const uint32_t low = sh.low;
   for (int i = (int)threadIdx.x; i < n; i += THREADS) {
     const uint64_t key = sh.key[i];
+    if ((uint32_t)(key >> 32) >= low) sh.near[atomicAdd(&sh.holders, 1)] = key;
+  }
+  __syncthreads();
+}
+
+// Calls out(rank, key) for the K largest of n keys, rank 0 the largest.  They
+// arrived in any order; they alone decide.
+template <int THREADS, class Out>
+__device__ __forceinline__ void top_ranked(const uint64_t* keys, int n, int K, const Out& out) {
+  for (int i = (int)threadIdx.x; i < n; i += THREADS) {
+    const uint64_t key = keys[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += sh.key[j] > key ? 1 : 0;
+    for (int j = 0; j < n; ++j) rank += keys[j] > key ? 1 : 0;
     if (rank < K) out(rank, key);
   }
 }

@@ -559,13 +559,11 @@ int qlora_norm_bwd(int64_t T, int64_t D, const uint16_t* dX, const void* h_out, 
  * -inf and entropy 0.  NaN or +inf makes its own row's log probabilities and
  * entropy NaN; among the alternatives NaN comes last.
  * Sums are fp32 and join in 64 bits.  Deterministic.
- * workspace: at least qlora_token_logprob_workspace_bytes, 16-byte aligned.
- * Errors: NULL, SHAPE, UNSUPPORTED (format, alignment, scale), WORKSPACE, HIP.
+ * Errors: NULL, SHAPE, UNSUPPORTED (format, alignment, scale), HIP.
  */
-int qlora_token_logprob_workspace_bytes(int64_t T, int64_t vocab, int32_t format, int32_t top, size_t* bytes);
 int qlora_token_logprob(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale,
                         int32_t n, const int64_t* tokens, float* logprob, float* stats, float* entropy, int32_t top,
-                        int64_t* top_ids, float* top_logprob, void* workspace, size_t workspace_bytes, void* stream);
+                        int64_t* top_ids, float* top_logprob, void* stream);
 
 /*
  * The gradient of the logits from d_logprob fp32 [T][n] and, or NULL,
@@ -611,10 +609,8 @@ int qlora_token_logprob_bwd(int64_t T, int64_t vocab, const void* logits, int32_
  * Rows, formats, alignment and errors as above (values, loss, stats and d_loss
  * 4-byte, ids 8-byte aligned).
  */
-int qlora_distill_workspace_bytes(int64_t T, int64_t vocab, int32_t format, size_t* bytes);
 int qlora_distill_fwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale, int32_t k,
-                      const int64_t* ids, const float* values, int32_t rest, float* loss, float* stats,
-                      void* workspace, size_t workspace_bytes, void* stream);
+                      const int64_t* ids, const float* values, int32_t rest, float* loss, float* stats, void* stream);
 int qlora_distill_bwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale, int32_t k,
                       const int64_t* ids, const float* values, int32_t rest, const float* stats, const float* d_loss,
                       void* dlogits, int64_t out_cols, int64_t out_ld, void* stream);

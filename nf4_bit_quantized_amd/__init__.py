@@ -72,10 +72,8 @@ EXPORTED = (
     "qlora_norm_fwd",
     "qlora_norm_bwd_workspace_bytes",
     "qlora_norm_bwd",
-    "qlora_token_logprob_workspace_bytes",
     "qlora_token_logprob",
     "qlora_token_logprob_bwd",
-    "qlora_distill_workspace_bytes",
     "qlora_distill_fwd",
     "qlora_distill_bwd",
     "qlora_adamw_step",
@@ -164,11 +162,9 @@ def lib() -> ctypes.CDLL:
     L.qlora_norm_bwd_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.qlora_norm_bwd.argtypes = [i64, i64, vp, vp, i32, vp, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz,
                                  vp]
-    L.qlora_token_logprob_workspace_bytes.argtypes = [i64, i64, i32, i32, ctypes.POINTER(sz)]
-    L.qlora_token_logprob.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.qlora_token_logprob.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, vp, vp, i32, vp, vp, vp]
     L.qlora_token_logprob_bwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, vp, vp, vp, vp, i64, i64, vp]
-    L.qlora_distill_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(sz)]
-    L.qlora_distill_fwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.qlora_distill_fwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, i32, vp, vp, vp]
     L.qlora_distill_bwd.argtypes = [i64, i64, vp, i32, i64, f32, i32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
     L.qlora_adamw_step.argtypes = [ctypes.POINTER(AdamwHparams), i64, vp, vp, vp, vp, vp, vp]
     L.qlora_trace_enable.argtypes = [ctypes.c_int]
@@ -1110,17 +1106,9 @@ def _entries(name: str, ids, T: int, what: str):
     return 1 if ids.dim() == 1 else ids.shape[1]
 
 
-@functools.lru_cache(maxsize=256)      # the sizes decide it
-def qlora_token_logprob_workspace_bytes(T: int, vocab: int, format: int, top: int = 0) -> int:
-    n = ctypes.c_size_t()
-    _check(lib().qlora_token_logprob_workspace_bytes(T, vocab, format, top, ctypes.byref(n)),
-           "qlora_token_logprob_workspace_bytes")
-    return n.value
-
-
 def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy: bool = False,
                         vocab: Optional[int] = None, logprob=None, stats=None, entropy=None, top_ids=None,
-                        top_logprob=None, workspace=None, stream=None):
+                        top_logprob=None, stream=None):
     """Log probabilities under softmax(scale * logits[:, :vocab]): returns (logprob, stats, entropy, top_ids,
     top_logprob), None for what was not asked.  logits float32, bfloat16 or float16 [T][columns], rows at any stride;
     tokens int64 [T] or [T][n], an entry outside 0 .. vocab - 1 (-100) has log probability 0; logprob float32 of
@@ -1139,8 +1127,7 @@ def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, w
     _check_out(entropy, (T,), torch.float32, "entropy")
     _check_out(top_ids, (T, top), torch.int64, "top_ids")
     _check_out(top_logprob, (T, top), torch.float32, "top_logprob")
-    device = _one_device(name, logits, tokens, logprob, stats, entropy, top_ids, top_logprob, workspace)
-    nbytes = qlora_token_logprob_workspace_bytes(T, vocab, fmt, top)
+    device = _one_device(name, logits, tokens, logprob, stats, entropy, top_ids, top_logprob)
     with _LaunchOn(device, stream, name) as st:
         if tokens is not None and logprob is None:
             logprob = torch.empty(tokens.shape, dtype=torch.float32, device=device)
@@ -1152,10 +1139,8 @@ def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, w
             top_ids = torch.empty((T, top), dtype=torch.int64, device=device)
         if top > 0 and top_logprob is None:
             top_logprob = torch.empty((T, top), dtype=torch.float32, device=device)
-        ws = _workspace(nbytes, device, workspace)
         _check(lib().qlora_token_logprob(T, vocab, _ptr(logits), fmt, ld, float(scale), n, _ptr(tokens), _ptr(logprob),
-                                         _ptr(stats), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprob), _ptr(ws),
-                                         nbytes, st), name)
+                                         _ptr(stats), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprob), st), name)
     return logprob, stats, entropy, top_ids, top_logprob
 
 
@@ -1198,13 +1183,6 @@ def qlora_token_logprob_bwd(logits, tokens, stats, d_logprob, scale: float = 1.0
     return dlogits
 
 
-@functools.lru_cache(maxsize=256)      # the sizes decide it
-def qlora_distill_workspace_bytes(T: int, vocab: int, format: int) -> int:
-    n = ctypes.c_size_t()
-    _check(lib().qlora_distill_workspace_bytes(T, vocab, format, ctypes.byref(n)), "qlora_distill_workspace_bytes")
-    return n.value
-
-
 def _teacher(name: str, ids, values, T: int) -> int:
     """k of a teacher's ids int64 and values float32, both [T][k]."""
     import torch
@@ -1216,7 +1194,7 @@ def _teacher(name: str, ids, values, T: int) -> int:
 
 
 def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = False, vocab: Optional[int] = None,
-                      loss=None, stats=None, workspace=None, stream=None):
+                      loss=None, stats=None, stream=None):
     """The distillation loss of each row, sum p (log p - log q), q = softmax(scale * logits[:, :vocab]): returns
     (loss float32 [T], stats float32 [T][4]).  p from the teacher's ids int64 [T][k] and values float32 [T][k] (its
     top_ids and top_logprob): softmax(values), or with rest=True exp(values) and what is left to 1 as one more
@@ -1227,16 +1205,14 @@ def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = Fals
     k = _teacher(name, ids, values, T)
     _check_out(loss, (T,), torch.float32, "loss")
     _check_out(stats, (T, 4), torch.float32, "stats")
-    device = _one_device(name, logits, ids, values, loss, stats, workspace)
-    nbytes = qlora_distill_workspace_bytes(T, vocab, fmt)
+    device = _one_device(name, logits, ids, values, loss, stats)
     with _LaunchOn(device, stream, name) as st:
         if loss is None:
             loss = torch.empty((T,), dtype=torch.float32, device=device)
         if stats is None:
             stats = torch.empty((T, 4), dtype=torch.float32, device=device)
-        ws = _workspace(nbytes, device, workspace)
         _check(lib().qlora_distill_fwd(T, vocab, _ptr(logits), fmt, ld, float(scale), k, _ptr(ids), _ptr(values),
-                                       1 if rest else 0, _ptr(loss), _ptr(stats), _ptr(ws), nbytes, st), name)
+                                       1 if rest else 0, _ptr(loss), _ptr(stats), st), name)
     return loss, stats
 
 

@@ -36,33 +36,21 @@ bool in_place_ok(const void* z, int64_t ld, const void* dz, int64_t out_ld) { re
 
 extern "C" {
 
-int qlora_token_logprob_workspace_bytes(int64_t T, int64_t vocab, int32_t format, int32_t top, size_t* bytes) {
-  if (!bytes) return QLORA_ERR_NULL;
-  const int st = check_rows(T, vocab, format, vocab, 1.0f);
-  if (st) return st;
-  if (!top_ok(top, vocab)) return QLORA_ERR_SHAPE;
-  *bytes = score_part_bytes(T, vocab, format, top);
-  return QLORA_OK;
-}
-
 int qlora_token_logprob(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale,
                         int32_t n, const int64_t* tokens, float* logprob, float* stats, float* entropy, int32_t top,
-                        int64_t* top_ids, float* top_logprob, void* workspace, size_t workspace_bytes, void* stream) {
+                        int64_t* top_ids, float* top_logprob, void* stream) {
   const int st = check_rows(T, vocab, format, ld, scale);
   if (st) return st;
   if (n < 0 || n > kLogitsMost || !top_ok(top, vocab)) return QLORA_ERR_SHAPE;
   if (T > 0 && (!logits || !stats || (n > 0 && (!tokens || !logprob)) || (top > 0 && (!top_ids || !top_logprob))))
     return QLORA_ERR_NULL;
   if (!aligned_to(logits, format_bytes(format)) || !aligned_to(tokens, 8) || !aligned4(logprob) ||
-      !aligned4(stats) || !aligned4(entropy) || !aligned_to(top_ids, 8) || !aligned4(top_logprob) ||
-      !aligned16(workspace))
+      !aligned4(stats) || !aligned4(entropy) || !aligned_to(top_ids, 8) || !aligned4(top_logprob))
     return QLORA_ERR_UNSUPPORTED;
-  const size_t need = score_part_bytes(T, vocab, format, top);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   ScoreParams P{};
   P.in = LogitsRows{logits, format, T, vocab, ld, scale};
   P.n = n; P.tokens = tokens; P.logprob = logprob; P.stats = stats; P.entropy = entropy;
-  P.top = top; P.top_ids = top_ids; P.top_logprob = top_logprob; P.part = workspace;
+  P.top = top; P.top_ids = top_ids; P.top_logprob = top_logprob;
   HIP_TRY(launch_score(P, (hipStream_t)stream));
   return QLORA_OK;
 }
@@ -89,30 +77,19 @@ int qlora_token_logprob_bwd(int64_t T, int64_t vocab, const void* logits, int32_
   return QLORA_OK;
 }
 
-int qlora_distill_workspace_bytes(int64_t T, int64_t vocab, int32_t format, size_t* bytes) {
-  if (!bytes) return QLORA_ERR_NULL;
-  const int st = check_rows(T, vocab, format, vocab, 1.0f);
-  if (st) return st;
-  *bytes = distill_part_bytes(T, vocab, format);
-  return QLORA_OK;
-}
-
 int qlora_distill_fwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale, int32_t k,
-                      const int64_t* ids, const float* values, int32_t rest, float* loss, float* stats,
-                      void* workspace, size_t workspace_bytes, void* stream) {
+                      const int64_t* ids, const float* values, int32_t rest, float* loss, float* stats, void* stream) {
   const int st = check_rows(T, vocab, format, ld, scale);
   if (st) return st;
   if (k < 1 || k > kLogitsMost) return QLORA_ERR_SHAPE;
   if (T > 0 && (!logits || !ids || !values || !loss || !stats)) return QLORA_ERR_NULL;
   if (!aligned_to(logits, format_bytes(format)) || !aligned_to(ids, 8) || !aligned4(values) || !aligned4(loss) ||
-      !aligned4(stats) || !aligned16(workspace))
+      !aligned4(stats))
     return QLORA_ERR_UNSUPPORTED;
-  const size_t need = distill_part_bytes(T, vocab, format);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   DistillParams P{};
   P.in = LogitsRows{logits, format, T, vocab, ld, scale};
   P.k = k; P.ids = ids; P.values = values; P.rest = rest != 0; P.loss = loss; P.stats = stats;
-  P.part = workspace;
+ 
   HIP_TRY(launch_distill(P, (hipStream_t)stream));
   return QLORA_OK;
 }

@@ -60,36 +60,36 @@ __device__ __forceinline__ void add(Sums& a, const float (&f)[N], float c) {
 // of piece p, in a window of kWindow pieces.
 constexpr int kWindow = 8192;
 
-template <int F, bool ENT, bool MASK, int THREADS>
+// U pieces to a thread at a time, all loads of a round before the first use;
+// the last round loads no further than the row.
+template <int F, bool ENT, bool MASK, int THREADS, int U>
 __device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first) {
-  constexpr int E = kPer<F>, U = 4;
-  int p = p0 + (int)threadIdx.x;
-  for (; p + (U - 1) * THREADS < p1; p += U * THREADS) {
+  constexpr int E = kPer<F>, N = U < 4 ? U : 4;
+  const auto round = [&](int p, auto all) {
     u32x4_t w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = row.load(p + u * THREADS);
-    float f[U * E];
+    for (int u = 0; u < U; ++u)
+      if (all.value || p + u * THREADS < p1) w[u] = row.load(p + u * THREADS);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      unpack<F>(w[u], f + u * E);
-      if constexpr (MASK) {
-        const uint32_t b = mask[p + u * THREADS - first];
-        if (b)
+    for (int v = 0; v < U; v += N) {
+      if (!all.value && p + v * THREADS >= p1) break;
+      float f[N * E];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const bool in = all.value || p + (u + v) * THREADS < p1;
+        unpack<F>(w[u + v], f + u * E);
+        const uint32_t b = !in ? 0xFFu : MASK ? mask[p + (u + v) * THREADS - first] : 0u;
+        if ((MASK || !all.value) && b) {
+#pragma unroll
           for (int e = 0; e < E; ++e) f[u * E + e] = (b >> e) & 1u ? kNone : f[u * E + e];
+        }
       }
+      add<N * E, ENT>(a, f, c);
     }
-    add<U * E, ENT>(a, f, c);
-  }
-  for (; p < p1; p += THREADS) {
-    float f[E];
-    unpack<F>(row.load(p), f);
-    if constexpr (MASK) {
-      const uint32_t b = mask[p - first];
-      if (b)
-        for (int e = 0; e < E; ++e) f[e] = (b >> e) & 1u ? kNone : f[e];
-    }
-    add<E, ENT>(a, f, c);
-  }
+  };
+  int p = p0 + (int)threadIdx.x;
+  for (; p + (U - 1) * THREADS < p1; p += U * THREADS) round(p, std::true_type());
+  if (p < p1) round(p, std::false_type());
 }
 
 struct Reduced {
@@ -133,8 +133,8 @@ __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double&
 
 // The statistics of pieces p0 .. p1 - 1 and, with `edges`, of the elements
 // outside the full pieces; every thread gets them.  With MASK the k elements of
-// ids are left out.
-template <int F, bool ENT, bool MASK, int THREADS>
+// ids (LDS) are left out.
+template <int F, bool ENT, bool MASK, int THREADS, int U>
 __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
                             uint32_t* mask, Reduced& sh, float* most = nullptr) {
   constexpr int E = kPer<F>;
@@ -163,7 +163,7 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
     }
   };
   Sums a;
-  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
+  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
   const int mine = edges && (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
   const float z_edge = mine >= 0 && !listed(mine) ? row.at(mine) : kNone;
   {
@@ -211,23 +211,25 @@ __device__ __forceinline__ float log_q(float z, float M, double scale, double lo
   return (float)(scale * ((double)z - (double)M) - log_s);
 }
 
-template <int F, bool ENT, int THREADS>
+template <int F, bool ENT, int THREADS, int U>
 __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   __shared__ Reduced red;
   __shared__ TopShared sh_top;
   const int64_t t = blockIdx.x;
   const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
+  // the given tokens' logits come with the row's first pieces, not behind its last
+  const int mine = (int)threadIdx.x;
+  const int64_t id = mine < P.n ? P.tokens[t * P.n + mine] : -1;
+  const bool given = id >= 0 && id < P.in.vocab;
+  const float z = given ? row.at(id) : 0.0f;
   float most;
-  const Stats r = statistics<F, ENT, false, THREADS>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
+  const Stats r = statistics<F, ENT, false, THREADS, U>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
   const double log_s = log(r.S), scale = (double)P.in.scale;
+  if (mine < P.n) P.logprob[t * P.n + mine] = given ? log_q(z, r.M, scale, log_s) : 0.0f;
   if (threadIdx.x == 0) {
     P.stats[2 * t] = r.M;
     P.stats[2 * t + 1] = (float)log_s;
     if constexpr (ENT) P.entropy[t] = r.S == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (r.T / r.S));
-  }
-  for (int i = (int)threadIdx.x; i < P.n; i += THREADS) {
-    const int64_t id = P.tokens[t * P.n + i];
-    P.logprob[t * P.n + i] = id >= 0 && id < P.in.vocab ? log_q(row.at(id), r.M, scale, log_s) : 0.0f;
   }
   if (P.top > 0) {
     top_candidates<F, THREADS>(row, row.full0, row.full1, true, P.top, most, sh_top);
@@ -248,26 +250,23 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
 // for the listed tokens, whole - ratio for the others (ratio = left / q_r).
 // Entries outside 0 .. vocab - 1 are left out; with none left, whole = 0.  Where
 // q_r = 0 the bucket is left out.
-template <int F, bool REST>
-__device__ void distill_finish(const DistillParams& P, int64_t t, const Row<F>& row, Stats r) {
-  const int lane = (int)threadIdx.x;
-  const double scale = (double)P.in.scale;
+struct Listed {  // two entries of a lane
   int64_t id[2];
   bool in[2];
-  double v[2];
-  float z[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 64 * h;
-    id[h] = i < P.k ? P.ids[t * P.k + i] : -1;
-    in[h] = id[h] >= 0 && id[h] < P.in.vocab;
-    v[h] = in[h] ? (double)P.values[t * P.k + i] : -__builtin_inf();
-    z[h] = in[h] ? row.at(id[h]) : kNone;
-  }
+  float v[2], z[2];
+};
+
+template <bool REST>
+__device__ void distill_finish(const DistillParams& P, int64_t t, const Listed& list, const int64_t* ids, Stats r) {
+  const int lane = (int)threadIdx.x;
+  const double scale = (double)P.in.scale;
+  const auto& in = list.in;
+  const auto& z = list.z;
+  double v[2] = {(double)list.v[0], (double)list.v[1]};
   const bool any = __ballot(in[0] || in[1]) != 0;
   double known = 0.0, log_known = 0.0;
   if constexpr (!REST) {
-    const double most = (double)wave::largest(fmaxf((float)v[0], (float)v[1]));
+    const double most = (double)wave::largest(fmaxf(list.v[0], list.v[1]));
     if (most > -__builtin_inf()) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) v[h] -= most;
@@ -279,9 +278,9 @@ __device__ void distill_finish(const DistillParams& P, int64_t t, const Row<F>& 
     // the listed elements join the sum, each token once
     bool first[2] = {in[0], in[1]};
     for (int j = 0; j < P.k; ++j) {
-      const int64_t other = P.ids[t * P.k + j];
-      first[0] = first[0] && !(j < lane && other == id[0]);
-      first[1] = first[1] && !(j < lane + 64 && other == id[1]);
+      const int64_t other = ids[j];
+      first[0] = first[0] && !(j < lane && other == list.id[0]);
+      first[1] = first[1] && !(j < lane + 64 && other == list.id[1]);
     }
     const float most = fmaxf(r.M, wave::largest(fmaxf(z[0], z[1])));
     if (most > kNone) {
@@ -328,56 +327,99 @@ __device__ void distill_finish(const DistillParams& P, int64_t t, const Row<F>& 
   }
 }
 
-template <int F, bool REST, int THREADS>
+template <int F, bool REST, int THREADS, int U>
 __global__ __launch_bounds__(THREADS) void k_distill(DistillParams P, float c) {
   __shared__ Reduced red;
   __shared__ uint32_t mask[REST ? kWindow / 4 : 1];
+  __shared__ int64_t ids[REST ? kLogitsMost : 1];
   const int64_t t = blockIdx.x;
   const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
-  const Stats r = statistics<F, false, REST, THREADS>(row, row.full0, row.full1, true, c, P.ids + t * P.k, P.k, mask, red);
-  if (threadIdx.x < 64) distill_finish<F, REST>(P, t, row, r);
+  // the entries and their logits come with the row's first pieces, not behind its last
+  Listed list;
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = (int)threadIdx.x + 64 * h;
+      list.id[h] = i < P.k ? P.ids[t * P.k + i] : -1;
+      list.in[h] = list.id[h] >= 0 && list.id[h] < P.in.vocab;
+      list.v[h] = list.in[h] ? P.values[t * P.k + i] : kNone;
+      list.z[h] = list.in[h] ? row.at(list.id[h]) : kNone;
+      if (REST && i < P.k) ids[i] = list.id[h];
+    }
+  }
+  if constexpr (REST) __syncthreads();
+  const Stats r = statistics<F, false, REST, THREADS, U>(row, row.full0, row.full1, true, c, ids, P.k, mask, red);
+  if (threadIdx.x < 64) distill_finish<REST>(P, t, list, ids, r);
 }
 
 float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634); }
 
-constexpr int kThreads = 512;
+// Threads to a row, from the row's bytes and the number of rows.  A thread
+// takes four pieces of 16 bytes at a time, so 256, 512 or 1024 threads want
+// 16, 32 or 64 KB of row a round, and what a last round leaves idle counts.  us
+// with 256, 512 and 1024 threads (statistics and one log probability, bf16):
+//   4096 x 16000   28.5  30.3  48.8        2048 x 64000   47.8  47.4  44.9
+//   4096 x 32000   49.3  47.3  62.7        2048 x 128256  89.9  89.5  85.4
+//   4096 x 50257   73.9  70.7  77.5        77 x 50257 (fp32, five alternatives)  14.4  9.5  12.1
+// Up to one row to a CU, 512 are faster than 1024 at any length.
+int row_threads(int64_t T, int64_t bytes) {
+  if (bytes < 48 << 10) return 256;
+  return T <= 256 || bytes < 112 << 10 ? 512 : 1024;
+}
+
+template <class Go>
+void by_format(int format, const Go& go) {
+  if (format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
+  else if (format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());
+  else go(std::integral_constant<int, kWeightF16>());
+}
+
+int64_t row_bytes(const LogitsRows& in) { return in.vocab * (in.format == kWeightF32 ? 4 : 2); }
 
 }  // namespace
 
-size_t score_part_bytes(int64_t, int64_t, int, int) { return 0; }
-size_t distill_part_bytes(int64_t, int64_t, int) { return 0; }
-
 hipError_t launch_score(const ScoreParams& P, hipStream_t stream) {
   if (P.in.T == 0) return hipSuccess;
-  KernelEvents ev(KID_LOGPROB);
-  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
   const float c = log2_scale(P.in.scale);
-  const dim3 grid((unsigned)P.in.T), block(kThreads);
-  const auto go = [&](auto f) {
+  const int threads = row_threads(P.in.T, row_bytes(P.in));
+  by_format(P.in.format, [&](auto f) {
     constexpr int F = decltype(f)::value;
-    if (P.entropy) hipExtLaunchKernelGGL((k_score<F, true, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
-    else hipExtLaunchKernelGGL((k_score<F, false, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
-  };
-  if (P.in.format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
-  else if (P.in.format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());
-  else go(std::integral_constant<int, kWeightF16>());
+    const auto go = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const dim3 grid((unsigned)P.in.T), block(N);
+      if (P.entropy) launch(KID_LOGPROB, k_score<F, true, N, 4>, grid, block, stream, P, c);
+      else launch(KID_LOGPROB, k_score<F, false, N, 4>, grid, block, stream, P, c);
+    };
+    if (threads == 256) go(std::integral_constant<int, 256>());
+    else if (threads == 512) go(std::integral_constant<int, 512>());
+    else go(std::integral_constant<int, 1024>());
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_distill(const DistillParams& P, hipStream_t stream) {
   if (P.in.T == 0) return hipSuccess;
-  KernelEvents ev(KID_DISTILL);
-  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
   const float c = log2_scale(P.in.scale);
-  const dim3 grid((unsigned)P.in.T), block(kThreads);
-  const auto go = [&](auto f) {
+  const int64_t bytes = row_bytes(P.in);
+  const int threads = row_threads(P.in.T, bytes);
+  by_format(P.in.format, [&](auto f) {
     constexpr int F = decltype(f)::value;
-    if (P.rest) hipExtLaunchKernelGGL((k_distill<F, true, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
-    else hipExtLaunchKernelGGL((k_distill<F, false, kThreads>), grid, block, 0, stream, e0, e1, 0, P, c);
-  };
-  if (P.in.format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
-  else if (P.in.format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());
-  else go(std::integral_constant<int, kWeightF16>());
+    const dim3 grid((unsigned)P.in.T);
+    if (P.rest) {
+      // the mask costs barriers, which small workgroups feel less.  us with 256 threads and four or eight pieces,
+      // 512 and 1024 with four: 4096 x 32000 55.0 63.4 70.9 108; 2048 x 64000 54.3 51.5 54.5 69.7; 2048 x 128256
+      // 102 96 97 111.  Few rows: 77 x 50257 (fp32) 19.1 16.2 14.2 15.6.
+      if (P.in.T <= 256 && threads >= 512) launch(KID_DISTILL, k_distill<F, true, 512, 4>, grid, dim3(512), stream, P, c);
+      else if (bytes < 112 << 10) launch(KID_DISTILL, k_distill<F, true, 256, 4>, grid, dim3(256), stream, P, c);
+      else launch(KID_DISTILL, k_distill<F, true, 256, 8>, grid, dim3(256), stream, P, c);
+    } else if (threads == 256) {
+      launch(KID_DISTILL, k_distill<F, false, 256, 4>, grid, dim3(256), stream, P, c);
+    } else if (threads == 512) {
+      launch(KID_DISTILL, k_distill<F, false, 512, 4>, grid, dim3(512), stream, P, c);
+    } else {
+      launch(KID_DISTILL, k_distill<F, false, 1024, 4>, grid, dim3(1024), stream, P, c);
+    }
+  });
   return hipGetLastError();
 }
 

@@ -28,9 +28,7 @@ struct ScoreParams {
   int top;
   int64_t* top_ids;       // [T][top]
   float* top_logprob;     // [T][top]
-  void* part;             // score_part_bytes
 };
-size_t score_part_bytes(int64_t T, int64_t vocab, int format, int top);
 hipError_t launch_score(const ScoreParams& p, hipStream_t stream);
 
 struct DistillParams {
@@ -41,9 +39,7 @@ struct DistillParams {
   int rest;
   float* loss;          // [T]
   float* stats;         // [T][4]
-  void* part;           // distill_part_bytes
 };
-size_t distill_part_bytes(int64_t T, int64_t vocab, int format);
 hipError_t launch_distill(const DistillParams& p, hipStream_t stream);
 
 // The gradient of either: n given tokens with their weights, or the teacher's k entries.

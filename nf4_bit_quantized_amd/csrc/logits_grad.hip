@@ -81,14 +81,23 @@ __device__ void entries(const LogitsGradParams& P, int64_t t, const Row<F>& row,
     float v[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) v[h] = in[h] ? P.values[t * P.n + lane + 64 * h] : kNone;
-    float most = 0.0f, k = 1.0f;
-    if (!P.rest) {
-      most = fmaxf(wave::largest(fmaxf(v[0], v[1])), -kMost);
-      k = wave::sum(expf(v[0] - most) + expf(v[1] - most));
+    float k = 1.0f;
+    if (P.rest) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = expf(v[h]);
+    } else {
+      const float most = fmaxf(wave::largest(fmaxf(v[0], v[1])), -kMost);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // v - most and what its rounding leaves (a far value's difference is off by its size times 2^-24)
+        const float d = v[h] - most, back = d - v[h], left = (v[h] - (d - back)) - (most + back), x = expf(d);
+        v[h] = x > 0.0f ? __builtin_fmaf(x, left, x) : 0.0f;
+      }
+      k = wave::sum(v[0] + v[1]);
       k = k > 0.0f ? 1.0f / k : 0.0f;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) w[h] = -g * (expf(v[h] - most) * k);
+    for (int h = 0; h < 2; ++h) w[h] = -g * (v[h] * k);
     A_listed = -g * whole;
     A = -g * (whole - ratio);
   } else {
@@ -183,13 +192,11 @@ int64_t logits_grad_groups(int64_t T, int64_t out_cols, int format) {
 
 hipError_t launch_logits_grad(const LogitsGradParams& P, hipStream_t stream) {
   if (P.in.T == 0) return hipSuccess;
-  KernelEvents ev(KID_LOGITS_GRAD);
-  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
   const int groups = (int)logits_grad_groups(1, P.out_cols, P.in.format);
   const dim3 grid((unsigned)(P.in.T * groups)), block(kThreads);
   const auto go = [&](auto f) {
     constexpr int F = decltype(f)::value;
-    hipExtLaunchKernelGGL((k_logits_grad<F>), grid, block, 0, stream, e0, e1, 0, P, groups);
+    launch(KID_LOGITS_GRAD, k_logits_grad<F>, grid, block, stream, P, groups);
   };
   if (P.in.format == kWeightF32) go(std::integral_constant<int, kWeightF32>());
   else if (P.in.format == kWeightBf16) go(std::integral_constant<int, kWeightBf16>());

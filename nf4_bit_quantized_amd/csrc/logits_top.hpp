@@ -20,16 +20,15 @@ __device__ __forceinline__ float top_value(uint64_t key) { return from_ordered((
 
 struct TopShared {
   uint64_t key[kCandidates];
-  uint64_t near[kCandidates];  // top_narrow's
   uint32_t most[256];          // keys of the groups of threads
   uint16_t who[1024];          // threads that hold candidates
   int count, holders;
   uint32_t low;
 };
 
-// The largest t with at least K of n keys (at most 64 * N) >= t, or one that
-// lets exactly K pass; 0 if there are fewer than K.  By one wave, bit by bit
-// from the top, `bits` of them: the bits below stay 0, and more may pass.
+// A limit that at least K of the wave's 64 * N keys reach: exactly K, or the
+// K-th largest with its last 32 - bits bits cleared; 0 if it has fewer than K
+// above 0.  Bit by bit from the top.
 template <int N>
 __device__ __forceinline__ uint32_t top_limit(const uint32_t (&key)[N], int K, int bits) {
   uint32_t t = 0;
@@ -157,41 +156,19 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
   if (sh.count > kCandidates) top_bisect<F, THREADS>(row, p0, p1, edges, K, (uint64_t)low << 32, ~(uint64_t)0, sh);
 }
 
-// Leaves of sh's candidates those that reach the K-th largest's first 32 bits.
-template <int THREADS>
-__device__ void top_narrow(int K, TopShared& sh) {
-  const int n = sh.count;
-  if (threadIdx.x < 64) {
-    uint32_t key[kCandidates / 64];
-#pragma unroll
-    for (int j = 0; j < kCandidates / 64; ++j) {
-      const int i = 64 * j + (int)threadIdx.x;
-      key[j] = i < n ? (uint32_t)(sh.key[i] >> 32) : 0u;
-    }
-    const uint32_t low = top_limit<kCandidates / 64>(key, K, 32);
-    if (threadIdx.x == 0) {
-      sh.low = low;
-      sh.holders = 0;
-    }
-  }
-  __syncthreads();
-  const uint32_t low = sh.low;
-  for (int i = (int)threadIdx.x; i < n; i += THREADS) {
-    const uint64_t key = sh.key[i];
-    if ((uint32_t)(key >> 32) >= low) sh.near[atomicAdd(&sh.holders, 1)] = key;
-  }
-  __syncthreads();
-}
-
 // Calls out(rank, key) for the K largest of n keys, rank 0 the largest.  They
-// arrived in any order; they alone decide.
+// arrived in any order; they alone decide.  Eight lanes to a key, each counting
+// the larger among an eighth of the others.
 template <int THREADS, class Out>
 __device__ __forceinline__ void top_ranked(const uint64_t* keys, int n, int K, const Out& out) {
-  for (int i = (int)threadIdx.x; i < n; i += THREADS) {
+  for (int i = (int)threadIdx.x >> 3; i < n; i += THREADS / 8) {
     const uint64_t key = keys[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > key ? 1 : 0;
-    if (rank < K) out(rank, key);
+    for (int j = (int)threadIdx.x & 7; j < n; j += 8) rank += keys[j] > key ? 1 : 0;
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);   // lane ^ 1
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);   // lane ^ 2
+    rank += __builtin_amdgcn_update_dpp(0, rank, 0x141, 0xF, 0xF, false);  // the other four of eight
+    if ((threadIdx.x & 7) == 0 && rank < K) out(rank, key);
   }
 }
 

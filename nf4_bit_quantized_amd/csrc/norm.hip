@@ -144,16 +144,14 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
 
 hipError_t launch_norm(const NormParams& P, hipStream_t stream) {
   if (P.T == 0) return hipSuccess;
-  KernelEvents ev(KID_NORM);
-  const hipEvent_t e0 = ev.start(), e1 = ev.stop();
   const int pieces = P.D / 8;
   const int np = pieces > 1024 ? 2 : 1;
   const int threads = ((pieces + np - 1) / np + 63) / 64 * 64;
   const dim3 grid((unsigned)P.T), block((unsigned)threads);
   const auto go = [&](auto fs, auto fw) {
     constexpr int FS = decltype(fs)::value, FW = decltype(fw)::value;
-    if (np == 1) hipExtLaunchKernelGGL((k_norm<FS, FW, 1>), grid, block, 0, stream, e0, e1, 0, P);
-    else hipExtLaunchKernelGGL((k_norm<FS, FW, 2>), grid, block, 0, stream, e0, e1, 0, P);
+    if (np == 1) launch(KID_NORM, k_norm<FS, FW, 1>, grid, block, stream, P);
+    else launch(KID_NORM, k_norm<FS, FW, 2>, grid, block, stream, P);
   };
   const std::integral_constant<int, kWeightF32> f32;
   const std::integral_constant<int, kWeightBf16> b16;

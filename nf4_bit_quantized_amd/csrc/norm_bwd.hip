@@ -204,17 +204,12 @@ hipError_t launch_norm_bwd(const NormParams& P, hipStream_t stream) {
   const int mode = !P.block ? 0 : P.post_weight ? 2 : 1;
   const auto go = [&](auto fs, auto fw, auto b) {
     constexpr int FS = decltype(fs)::value, FW = decltype(fw)::value, B = decltype(b)::value;
-    {
-      KernelEvents ev(KID_NORM_BWD);
-      const hipEvent_t e0 = ev.start(), e1 = ev.stop();
-      const dim3 grid((unsigned)groups), block((unsigned)threads);
-      if (np == 1) hipExtLaunchKernelGGL((k_norm_bwd<FS, FW, 1, B>), grid, block, 0, stream, e0, e1, 0, P);
-      else hipExtLaunchKernelGGL((k_norm_bwd<FS, FW, 2, B>), grid, block, 0, stream, e0, e1, 0, P);
-    }
+    const dim3 grid((unsigned)groups), block((unsigned)threads);
+    if (np == 1) launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B>, grid, block, stream, P);
+    else launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 2, B>, grid, block, stream, P);
     if (P.dweight) {
-      KernelEvents ev(KID_NORM_SUM);
-      const dim3 grid((unsigned)(P.D / 64), P.dgate || P.dpost_weight ? 2 : 1);
-      hipExtLaunchKernelGGL((k_norm_sum<FW>), grid, dim3(256), 0, stream, ev.start(), ev.stop(), 0, P, groups);
+      const dim3 sums((unsigned)(P.D / 64), P.dgate || P.dpost_weight ? 2 : 1);
+      launch(KID_NORM_SUM, k_norm_sum<FW>, sums, dim3(256), stream, P, groups);
     }
   };
   const std::integral_constant<int, kWeightF32> f32;

@@ -70,4 +70,13 @@ class KernelEvents {
   hipEvent_t start_ = nullptr, stop_ = nullptr;
 };
 
+// Launches a kernel of kind kid, timed as above if it is traced.  Untimed, the
+// plain launch takes 0.7 us less of host time than hipExtLaunchKernelGGL.
+template <class... Params, class... Args>
+void launch(int kid, void (*kernel)(Params...), dim3 grid, dim3 block, hipStream_t stream, Args... args) {
+  KernelEvents ev(kid);
+  if (ev.start()) hipExtLaunchKernelGGL(kernel, grid, block, 0, stream, ev.start(), ev.stop(), 0, args...);
+  else hipLaunchKernelGGL(kernel, grid, block, 0, stream, args...);
+}
+
 }  // namespace qlora

@@ -111,7 +111,9 @@ def distill(z, scale, ids, values, rest):
 
 
 def distill_gradient(z, scale, ids, values, rest, d_loss, M, log_s, whole, ratio):
-    """(gradient, magnitude) of one row, from its statistics."""
+    """(gradient, magnitude) of one row, from its statistics.  p counts twice: in 32 bits it is an exponential (two
+    half steps and one), a sum of at most 128 of them in a tree (eight), its reciprocal and two products: fourteen half
+    steps, where a magnitude's measure, 2^-21, has eight."""
     z = np.asarray(z, np.float64)
     V = len(z)
     in_, _, p, _ = _teacher(ids, values, V, rest)
@@ -126,4 +128,4 @@ def distill_gradient(z, scale, ids, values, rest, d_loss, M, log_s, whole, ratio
     lq = np.where(q == 0, 0.0, lq)
     share = np.where(listed, whole, whole - ratio)
     size = np.where(listed, whole, whole + ratio)
-    return scale * d_loss * (share * q - w), scale * abs(d_loss) * (w + q * size * (4 + np.abs(lq)))
+    return scale * d_loss * (share * q - w), scale * abs(d_loss) * (2 * w + q * size * (4 + np.abs(lq)))

@@ -68,23 +68,15 @@ ROWS = [(0, -1, SHAPE), (0, 1 << 22, SHAPE), (1, 0, SHAPE), (1, 1 << 31, SHAPE),
 
 def test_logprob_arguments():
     L = q.lib()
-    n = ctypes.c_size_t()
-    assert L.qlora_token_logprob_workspace_bytes(4, 100, 1, 5, ctypes.byref(n)) == OK
-    need = n.value
-    #       0  1    2  3  4    5    6  7  8  9  10 11 12 13 14 15    16
-    good = [4, 100, F, 1, 100, 1.0, 2, F, F, F, F, 5, F, F, F, need, None]
+    #       0  1    2  3  4    5    6  7  8  9  10 11 12 13 14
+    good = [4, 100, F, 1, 100, 1.0, 2, F, F, F, F, 5, F, F, None]
     wrong = ROWS + [(6, -1, SHAPE), (6, 129, SHAPE), (11, -1, SHAPE), (11, 101, SHAPE), (11, 129, SHAPE),
                     (7, None, NULL), (8, None, NULL), (9, None, NULL), (12, None, NULL), (13, None, NULL),
                     (7, F + 4, UNSUP), (8, F + 2, UNSUP), (9, F + 2, UNSUP), (10, F + 1, UNSUP), (12, F + 4, UNSUP),
-                    (13, F + 2, UNSUP), (14, F + 8, UNSUP)]
-    if need:
-        wrong += [(14, None, WS), (15, need - 1, WS)]
+                    (13, F + 2, UNSUP)]
     for args, want in _each_wrong(good, wrong):
         assert L.qlora_token_logprob(*args) == want, args
-    assert L.qlora_token_logprob(0, 100, None, 1, 100, 1.0, 2, None, None, None, None, 5, None, None, None, 0, None) == OK
-    for args, want in (((4, 100, 1, 5, None), NULL), ((4, 100, 1, 101, ctypes.byref(n)), SHAPE),
-                       ((4, 0, 1, 0, ctypes.byref(n)), SHAPE), ((4, 100, 5, 0, ctypes.byref(n)), UNSUP)):
-        assert L.qlora_token_logprob_workspace_bytes(*args) == want
+    assert L.qlora_token_logprob(0, 100, None, 1, 100, 1.0, 2, None, None, None, None, 5, None, None, None) == OK
 
 
 def test_logprob_backward_arguments():
@@ -108,19 +100,12 @@ def test_logprob_backward_arguments():
 
 def test_distill_arguments():
     L = q.lib()
-    n = ctypes.c_size_t()
-    assert L.qlora_distill_workspace_bytes(4, 100, 1, ctypes.byref(n)) == OK
-    need = n.value
-    #       0  1    2  3  4    5    6  7  8  9  10 11 12 13    14
-    good = [4, 100, F, 1, 100, 1.0, 3, F, F, 0, F, F, F, need, None]
+    #       0  1    2  3  4    5    6  7  8  9  10 11 12
+    good = [4, 100, F, 1, 100, 1.0, 3, F, F, 0, F, F, None]
     wrong = ROWS + [(6, 0, SHAPE), (6, 129, SHAPE), (7, None, NULL), (8, None, NULL), (10, None, NULL), (11, None, NULL),
-                    (7, F + 4, UNSUP), (8, F + 2, UNSUP), (10, F + 2, UNSUP), (11, F + 2, UNSUP), (12, F + 8, UNSUP)]
-    if need:
-        wrong += [(12, None, WS), (13, need - 1, WS)]
+                    (7, F + 4, UNSUP), (8, F + 2, UNSUP), (10, F + 2, UNSUP), (11, F + 2, UNSUP)]
     for args, want in _each_wrong(good, wrong):
         assert L.qlora_distill_fwd(*args) == want, args
-    assert L.qlora_distill_workspace_bytes(4, 100, 1, None) == NULL
-    assert L.qlora_distill_workspace_bytes(-1, 100, 1, ctypes.byref(n)) == SHAPE
     #       0  1    2  3  4    5    6  7  8  9  10 11 12      13   14   15
     good = [4, 100, F, 1, 100, 1.0, 3, F, F, 0, F, F, F + 64, 100, 100, None]
     wrong = ROWS + [(6, 0, SHAPE), (6, 129, SHAPE), (13, 99, SHAPE), (14, 99, SHAPE), (7, None, NULL), (8, None, NULL),

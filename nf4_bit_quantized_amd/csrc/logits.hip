@@ -62,14 +62,14 @@ constexpr int kWindow = 8192;
 
 // U pieces to a thread at a time, all loads of a round before the first use;
 // the last round loads no further than the row.
-template <int F, bool ENT, bool MASK, int THREADS, int U>
+template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
 __device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first) {
   constexpr int E = kPer<F>, N = U < 4 ? U : 4;
   const auto round = [&](int p, auto all) {
     u32x4_t w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (all.value || p + u * THREADS < p1) w[u] = row.load(p + u * THREADS);
+      if (all.value || p + u * THREADS < p1) w[u] = row.template load<PAST>(p + u * THREADS);
 #pragma unroll
     for (int v = 0; v < U; v += N) {
       if (!all.value && p + v * THREADS >= p1) break;
@@ -134,7 +134,7 @@ __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double&
 // The statistics of pieces p0 .. p1 - 1 and, with `edges`, of the elements
 // outside the full pieces; every thread gets them.  With MASK the k elements of
 // ids (LDS) are left out.
-template <int F, bool ENT, bool MASK, int THREADS, int U>
+template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
 __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
                             uint32_t* mask, Reduced& sh, float* most = nullptr) {
   constexpr int E = kPer<F>;
@@ -163,7 +163,7 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
     }
   };
   Sums a;
-  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
+  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U, PAST>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
   const int mine = edges && (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
   const float z_edge = mine >= 0 && !listed(mine) ? row.at(mine) : kNone;
   {
@@ -211,7 +211,7 @@ __device__ __forceinline__ float log_q(float z, float M, double scale, double lo
   return (float)(scale * ((double)z - (double)M) - log_s);
 }
 
-template <int F, bool ENT, int THREADS, int U>
+template <int F, bool ENT, int THREADS, int U, bool PAST>
 __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   __shared__ Reduced red;
   __shared__ TopShared sh_top;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   const bool given = id >= 0 && id < P.in.vocab;
   const float z = given ? row.at(id) : 0.0f;
   float most;
-  const Stats r = statistics<F, ENT, false, THREADS, U>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
+  const Stats r = statistics<F, ENT, false, THREADS, U, PAST>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
   const double log_s = log(r.S), scale = (double)P.in.scale;
   if (mine < P.n) P.logprob[t * P.n + mine] = given ? log_q(z, r.M, scale, log_s) : 0.0f;
   if (threadIdx.x == 0) {
@@ -327,7 +327,7 @@ __device__ void distill_finish(const DistillParams& P, int64_t t, const Listed& 
   }
 }
 
-template <int F, bool REST, int THREADS, int U>
+template <int F, bool REST, int THREADS, int U, bool PAST>
 __global__ __launch_bounds__(THREADS) void k_distill(DistillParams P, float c) {
   __shared__ Reduced red;
   __shared__ uint32_t mask[REST ? kWindow / 4 : 1];
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(DistillParams P, float c) {
     }
   }
   if constexpr (REST) __syncthreads();
-  const Stats r = statistics<F, false, REST, THREADS, U>(row, row.full0, row.full1, true, c, ids, P.k, mask, red);
+  const Stats r = statistics<F, false, REST, THREADS, U, PAST>(row, row.full0, row.full1, true, c, ids, P.k, mask, red);
   if (threadIdx.x < 64) distill_finish<REST>(P, t, list, ids, r);
 }
 
@@ -374,25 +374,35 @@ void by_format(int format, const Go& go) {
   else go(std::integral_constant<int, kWeightF16>());
 }
 
-int64_t row_bytes(const LogitsRows& in) { return in.vocab * (in.format == kWeightF32 ? 4 : 2); }
+// Alternatives read pieces of the row a second time, from the caches.
+// 4096 x 128256 bf16 (1.05 GB) after their gradients were written: 154 us past
+// the caches, 174 through them; 2048 x 128256 with 64 alternatives 115 and 112.
+bool read_past(const LogitsRows& in, int top) { return top == 0 && in.T * in.bytes() >= kCacheBytes; }
 
 }  // namespace
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 hipError_t launch_score(const ScoreParams& P, hipStream_t stream) {
   if (P.in.T == 0) return hipSuccess;
   const float c = log2_scale(P.in.scale);
-  const int threads = row_threads(P.in.T, row_bytes(P.in));
+  const int threads = row_threads(P.in.T, P.in.bytes());
   by_format(P.in.format, [&](auto f) {
-    constexpr int F = decltype(f)::value;
-    const auto go = [&](auto n) {
-      constexpr int N = decltype(n)::value;
+    const auto go = [&](auto n, auto past) {
+      constexpr int F = decltype(f)::value, N = decltype(n)::value;
+      constexpr bool PAST = decltype(past)::value;
       const dim3 grid((unsigned)P.in.T), block(N);
-      if (P.entropy) launch(KID_LOGPROB, k_score<F, true, N, 4>, grid, block, stream, P, c);
-      else launch(KID_LOGPROB, k_score<F, false, N, 4>, grid, block, stream, P, c);
+      if (P.entropy) launch(KID_LOGPROB, k_score<F, true, N, 4, PAST>, grid, block, stream, P, c);
+      else launch(KID_LOGPROB, k_score<F, false, N, 4, PAST>, grid, block, stream, P, c);
     };
-    if (threads == 256) go(std::integral_constant<int, 256>());
-    else if (threads == 512) go(std::integral_constant<int, 512>());
-    else go(std::integral_constant<int, 1024>());
+    const auto by_threads = [&](auto past) {
+      if (threads == 256) go(Int<256>(), past);
+      else if (threads == 512) go(Int<512>(), past);
+      else go(Int<1024>(), past);
+    };
+    if (read_past(P.in, P.top)) by_threads(std::true_type());
+    else by_threads(std::false_type());
   });
   return hipGetLastError();
 }
@@ -400,25 +410,32 @@ hipError_t launch_score(const ScoreParams& P, hipStream_t stream) {
 hipError_t launch_distill(const DistillParams& P, hipStream_t stream) {
   if (P.in.T == 0) return hipSuccess;
   const float c = log2_scale(P.in.scale);
-  const int64_t bytes = row_bytes(P.in);
+  const int64_t bytes = P.in.bytes();
   const int threads = row_threads(P.in.T, bytes);
   by_format(P.in.format, [&](auto f) {
-    constexpr int F = decltype(f)::value;
-    const dim3 grid((unsigned)P.in.T);
-    if (P.rest) {
-      // the mask costs barriers, which small workgroups feel less.  us with 256 threads and four or eight pieces,
-      // 512 and 1024 with four: 4096 x 32000 55.0 63.4 70.9 108; 2048 x 64000 54.3 51.5 54.5 69.7; 2048 x 128256
-      // 102 96 97 111.  Few rows: 77 x 50257 (fp32) 19.1 16.2 14.2 15.6.
-      if (P.in.T <= 256 && threads >= 512) launch(KID_DISTILL, k_distill<F, true, 512, 4>, grid, dim3(512), stream, P, c);
-      else if (bytes < 112 << 10) launch(KID_DISTILL, k_distill<F, true, 256, 4>, grid, dim3(256), stream, P, c);
-      else launch(KID_DISTILL, k_distill<F, true, 256, 8>, grid, dim3(256), stream, P, c);
-    } else if (threads == 256) {
-      launch(KID_DISTILL, k_distill<F, false, 256, 4>, grid, dim3(256), stream, P, c);
-    } else if (threads == 512) {
-      launch(KID_DISTILL, k_distill<F, false, 512, 4>, grid, dim3(512), stream, P, c);
-    } else {
-      launch(KID_DISTILL, k_distill<F, false, 1024, 4>, grid, dim3(1024), stream, P, c);
-    }
+    const auto go = [&](auto rest, auto n, auto u, auto past) {
+      constexpr int F = decltype(f)::value, N = decltype(n)::value, U = decltype(u)::value;
+      launch(KID_DISTILL, k_distill<F, decltype(rest)::value, N, U, decltype(past)::value>, dim3((unsigned)P.in.T), dim3(N),
+             stream, P, c);
+    };
+    const auto by_threads = [&](auto past) {
+      if (P.rest) {
+        // the mask costs barriers, which small workgroups feel less.  us with 256 threads and four or eight pieces,
+        // 512 and 1024 with four: 4096 x 32000 55.0 63.4 70.9 108; 2048 x 64000 54.3 51.5 54.5 69.7; 2048 x 128256
+        // 102 96 97 111.  Few rows: 77 x 50257 (fp32) 19.1 16.2 14.2 15.6.
+        if (P.in.T <= 256 && threads >= 512) go(std::true_type(), Int<512>(), Int<4>(), past);
+        else if (bytes < 112 << 10) go(std::true_type(), Int<256>(), Int<4>(), past);
+        else go(std::true_type(), Int<256>(), Int<8>(), past);
+      } else if (threads == 256) {
+        go(std::false_type(), Int<256>(), Int<4>(), past);
+      } else if (threads == 512) {
+        go(std::false_type(), Int<512>(), Int<4>(), past);
+      } else {
+        go(std::false_type(), Int<1024>(), Int<4>(), past);
+      }
+    };
+    if (read_past(P.in, 0)) by_threads(std::true_type());
+    else by_threads(std::false_type());
   });
   return hipGetLastError();
 }

@@ -16,7 +16,12 @@ struct LogitsRows {
   int format;      // kWeight*
   int64_t T, vocab, ld;
   float scale;     // q = softmax(scale * z)
+  int64_t bytes() const { return vocab * (format == kWeightF32 ? 4 : 2); }  // of a row
 };
+
+// The last-level cache of the card.  Logits that it does not hold gain nothing
+// from passing through it, and push out what others left there.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 
 struct ScoreParams {
   LogitsRows in;
@@ -123,8 +128,11 @@ struct Row {
     full1 = (int)(end / kPer<F>);
     if (full1 < full0) full1 = full0;
   }
+  template <bool PAST = false>  // not kept in the caches
   __device__ __forceinline__ u32x4_t load(int p) const {
-    return *reinterpret_cast<const u32x4_t*>(aligned + (int64_t)p * 16);
+    const u32x4_t* const q = reinterpret_cast<const u32x4_t*>(aligned + (int64_t)p * 16);
+    if constexpr (PAST) return __builtin_nontemporal_load(q);
+    return *q;
   }
   __device__ __forceinline__ float at(int64_t i) const { return element<F>(start, i); }
   // The elements outside the full pieces: [0, edge0) and [edge1, vocab), fewer than 2 * kPer.

@@ -5,11 +5,17 @@
 //          = r_b (post_weight dp - m mean(post_weight dp m))
 //   dweight = sum_t dx n;  with C = sum_t dh m
 //   dgate = scale post_weight C,  dpost_weight = scale gate C
+// The two means come from sums that need no other mean, in one reduction: with
+// c = scale gate post_weight,
+//   sum c dh m = sum c m (dh' + r weight dx) - r mean(weight dx n) sum c m n
 // A workgroup owns every G-th token and a thread the same eight (or twice
 // eight) channels of all of them, so the sums over tokens stay in its registers
-// until the end; the workgroups' sums are then added in their order by a second
-// kernel (no atomics).  dx, h', dh' and block are read once, dh and dblock
-// written once.
+// until the end, and the next token's pieces load while this one's are summed;
+// the workgroups' sums are then added in their order by a second kernel (no
+// atomics).  dx, h', dh' and block are read once, dh and dblock written once.
+// Bound by HBM: 4096 x 8192 bf16 (335 MB) in 60 + 4 us, 5.2 TB/s; with a norm
+// behind the block and a gate (403 MB) 78 + 5; 1333 x 4096 in fp32 with both (98
+// MB) 20 + 5.
 #include <type_traits>
 
 #include "norm.hpp"
@@ -21,125 +27,169 @@ namespace {
 
 using namespace norm;
 
-constexpr int kGroups = 256;
+// What the call reads of a block: nothing of it where it has neither a norm nor
+// a gate's gradient, whose dblock is a multiple of dh.
+enum Block { kNoBlock, kPlainBlock, kGatedBlock, kNormedBlock };
 
-__device__ __forceinline__ float block_sum(float v, float* slot) {
-  v = wave::sum(v);
-  const int waves = (int)blockDim.x >> 6;
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < waves; ++w) s += slot[w];
-  return s;
+template <int FS, int B>
+struct Token {
+  Eight<kWeightBf16> dx, block;
+  Eight<FS> h, later;
+  __device__ __forceinline__ void load(const NormParams& P, int64_t i, bool in) {
+    if (!in) {
+      dx.zero();
+      h.zero();
+      later.zero();
+      block.zero();
+      return;
+    }
+    dx.load(P.dx, i);
+    h.load(P.h_out, i);
+    if (P.dh_out) later.load(P.dh_out, i);
+    else later.zero();
+    if constexpr (B >= kGatedBlock) block.load(P.block, i);
+  }
+};
+
+// weight and c = scale gate post_weight of a thread's eight channels
+template <int FW, int B>
+__device__ __forceinline__ void factors(const NormParams& P, int p, bool in, float (&w)[8], float (&c)[8]) {
+  Eight<FW> t;
+  t.zero();
+  if (in) t.load(P.weight, 8 * p);
+  t.values(w);
+  if constexpr (B > kNoBlock) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = P.scale;
+    float v[8];
+    if (P.gate && in) {
+      t.load(P.gate, 8 * p);
+      t.values(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] *= v[e];
+    }
+    if (B == kNormedBlock && in) {
+      t.load(P.post_weight, 8 * p);
+      t.values(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] *= v[e];
+    }
+  }
 }
 
-template <int F>
-__device__ __forceinline__ void values_at(const void* p, int64_t i, bool in, float (&f)[8]) {
-  Eight<F> v;
-  v.zero();
-  if (in) v.load(p, i);
-  v.values(f);
-}
-
-// BLOCK: 0 none, 1 a block, 2 a block with a norm behind it
-template <int FS, int FW, int NP, int BLOCK>
+// NP: pieces of eight channels a thread holds.  With one, its factors stay in
+// registers and the next token's pieces are on their way; with two (more than
+// 8192 channels) there is no room for either.
+template <int FS, int FW, int NP, int B>
 __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
-  __shared__ float slot[2][2][16];  // by token in turn: the one before may still be read
-  const int pieces = P.D / 8, step = (int)blockDim.x;
+  __shared__ float4 slot[2][16];  // by token in turn: the one before may still be read
+  const int pieces = P.D / 8, step = (int)blockDim.x, tid = (int)threadIdx.x, waves = step >> 6;
   float dw[NP][8], dc[NP][8];
 #pragma unroll
   for (int u = 0; u < NP; ++u)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[u][e] = dc[u][e] = 0.0f;
+  float w[8], c[8];
+  if constexpr (NP == 1) factors<FW, B>(P, tid, tid < pieces, w, c);
   const float inv = 1.0f / (float)P.D;
+  Token<FS, B> now[NP], next[NP];
+  float2 r_now = {}, r_next = {};
+  const auto load = [&](int64_t t, Token<FS, B>(&to)[NP], float2& r) {
+#pragma unroll
+    for (int u = 0; u < NP; ++u) to[u].load(P, t * P.D + 8 * (u * step + tid), u * step + tid < pieces);
+    r = float2{P.stats[2 * t], P.stats[2 * t + 1]};
+  };
+  if constexpr (NP == 1) load(blockIdx.x, next, r_next);
   int turn = 0;
   for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
-    const int64_t base = t * P.D;
-    const float r = P.stats[2 * t], r_b = BLOCK == 2 ? P.stats[2 * t + 1] : 1.0f;
-    float dn[NP][8], n[NP][8], s = 0.0f;
+    if constexpr (NP == 1) {
+      now[0] = next[0];
+      r_now = r_next;
+      if (t + gridDim.x < P.T) load(t + gridDim.x, next, r_next);
+    } else {
+      load(t, now, r_now);
+    }
+    const float r = r_now.x, r_b = B == kNormedBlock ? r_now.y : 1.0f;
+    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const int p = u * step + (int)threadIdx.x;
-      const bool in = p < pieces;
-      float dx[8], w[8];
-      values_at<kWeightBf16>(P.dx, base + 8 * p, in, dx);
-      values_at<FS>(P.h_out, base + 8 * p, in, n[u]);
-      values_at<FW>(P.weight, 8 * p, in, w);
+      float dx[8], n[8], later[8], m[8];
+      if constexpr (NP > 1) factors<FW, B>(P, u * step + tid, u * step + tid < pieces, w, c);
+      now[u].dx.values(dx);
+      now[u].h.values(n);
+      if constexpr (B == kNormedBlock) {
+        now[u].later.values(later);
+        now[u].block.values(m);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[u][e] *= r;
-        dw[u][e] = __builtin_fmaf(dx[e], n[u][e], dw[u][e]);
-        dn[u][e] = dx[e] * w[e];
-        s = __builtin_fmaf(dn[u][e], n[u][e], s);
+        n[e] *= r;
+        const float dn = dx[e] * w[e];
+        s1 = __builtin_fmaf(dn, n[e], s1);
+        if constexpr (B == kNormedBlock) {
+          const float cm = c[e] * m[e];
+          s2 = __builtin_fmaf(cm, __builtin_fmaf(r, dn, later[e]), s2);
+          s3 = __builtin_fmaf(cm, n[e], s3);
+        }
       }
     }
-    const float mean = block_sum(s, slot[turn][0]) * inv;
-    float sp = 0.0f;
+    s1 = wave::sum(s1);
+    if constexpr (B == kNormedBlock) {
+      s2 = wave::sum(s2);
+      s3 = wave::sum(s3);
+    }
+    if (waves > 1) {
+      if ((tid & 63) == 0) slot[turn][tid >> 6] = float4{s1, s2, s3, 0.0f};
+      __syncthreads();
+      s1 = s2 = s3 = 0.0f;
+      for (int v = 0; v < waves; ++v) {
+        const float4 x = slot[turn][v];
+        s1 += x.x;
+        s2 += x.y;
+        s3 += x.z;
+      }
+    }
+    const float mean = s1 * inv;
+    const float mean_p = r_b * r_b * r_b * inv * __builtin_fmaf(-r * mean, s3, s2);  // r_b of c dh m, of m and of dblock
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const int p = u * step + (int)threadIdx.x;
+      const int p = u * step + tid;
       const bool in = p < pieces;
-      float d[8];
-      if (P.dh_out) {
-        values_at<FS>(P.dh_out, base + 8 * p, in, d);
-      } else {
+      float dx[8], n[8], d[8];
+      if constexpr (NP > 1) factors<FW, B>(P, p, in, w, c);
+      now[u].dx.values(dx);
+      now[u].h.values(n);
+      now[u].later.values(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        n[e] *= r;
+        dw[u][e] = __builtin_fmaf(dx[e], n[e], dw[u][e]);
+        d[e] = __builtin_fmaf(r, __builtin_fmaf(-mean, n[e], dx[e] * w[e]), d[e]);
       }
+      if (in) store8<FS>(P.dh, t * P.D + 8 * p, d);
+      if constexpr (B > kNoBlock) {
+        float m[8];
+        if constexpr (B >= kGatedBlock) {
+          now[u].block.values(m);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = __builtin_fmaf(r, __builtin_fmaf(-mean, n[u][e], dn[u][e]), d[e]);
-      if (in) store8<FS>(P.dh, base + 8 * p, d);
-      if constexpr (BLOCK > 0) {
-        float g[8], w[8];
-        if (P.gate) {
-          values_at<FW>(P.gate, 8 * p, in, g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= P.scale;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = P.scale;
+          for (int e = 0; e < 8; ++e) dc[u][e] = __builtin_fmaf(d[e], m[e] * r_b, dc[u][e]);
         }
-        if (BLOCK == 2 || (P.dgate && P.dweight)) {
-          // n holds m, dn the gradient of m from here on
-          values_at<kWeightBf16>(P.block, base + 8 * p, in, n[u]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            n[u][e] *= r_b;
-            dc[u][e] = __builtin_fmaf(d[e], n[u][e], dc[u][e]);
-          }
-        }
-        if constexpr (BLOCK == 2) values_at<FW>(P.post_weight, 8 * p, in, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dn[u][e] = d[e] * g[e];
-          if constexpr (BLOCK == 2) {
-            dn[u][e] *= w[e];
-            sp = __builtin_fmaf(dn[u][e], n[u][e], sp);
-          }
+          d[e] *= c[e];
+          if constexpr (B == kNormedBlock) d[e] = __builtin_fmaf(-mean_p, m[e], r_b * d[e]);
         }
-        if constexpr (BLOCK == 1)
-          if (in) store8<kWeightBf16>(P.dblock, base + 8 * p, dn[u]);
-      }
-    }
-    if constexpr (BLOCK == 2) {
-      const float mean_p = block_sum(sp, slot[turn][1]) * inv;
-#pragma unroll
-      for (int u = 0; u < NP; ++u) {
-        const int p = u * step + (int)threadIdx.x;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dn[u][e] = r_b * __builtin_fmaf(-mean_p, n[u][e], dn[u][e]);
-        if (p < pieces) store8<kWeightBf16>(P.dblock, base + 8 * p, dn[u]);
+        if (in) store8<kWeightBf16>(P.dblock, t * P.D + 8 * p, d);
       }
     }
   }
   if (!P.dweight) return;
 #pragma unroll
   for (int u = 0; u < NP; ++u) {
-    const int p = u * step + (int)threadIdx.x;
+    const int p = u * step + tid;
     if (p >= pieces) continue;
     store8<kWeightF32>(P.part, (2 * (int64_t)blockIdx.x) * P.D + 8 * p, dw[u]);
-    if (BLOCK > 0) store8<kWeightF32>(P.part, (2 * (int64_t)blockIdx.x + 1) * P.D + 8 * p, dc[u]);
+    if (B >= kGatedBlock) store8<kWeightF32>(P.part, (2 * (int64_t)blockIdx.x + 1) * P.D + 8 * p, dc[u]);
   }
 }
 
@@ -190,37 +240,46 @@ __global__ __launch_bounds__(256) void k_norm_sum(NormParams P, int groups) {
   }
 }
 
-}  // namespace
-
-size_t norm_bwd_part_bytes(int64_t T, int64_t D) {
-  return (size_t)((T < kGroups ? T : kGroups) * 2 * D * (int64_t)sizeof(float));
+// Threads of a workgroup, and workgroups: two to a CU up to 4096 channels, one
+// above, each with the same number of tokens or one less.  us of both kernels
+// with one, two and four to a CU: 8192 x 2048 normed 45 42 44; 4096 x 4096 36 33
+// 35; 8192 x 1024 (fp32, normed; two, four and eight) 36 37 39.  With one and
+// two, 4096 x 8192: 65 67.
+int bwd_threads(int64_t D) { return (int)((D / 8 / (D > 8192 ? 2 : 1) + 63) / 64 * 64); }
+int64_t bwd_groups(int64_t T, int64_t D) {
+  const int64_t most = D <= 4096 ? 512 : 256, turns = (T + most - 1) / most;
+  return turns ? (T + turns - 1) / turns : 0;
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+}  // namespace
+
+size_t norm_bwd_part_bytes(int64_t T, int64_t D) { return (size_t)(bwd_groups(T, D) * 2 * D * (int64_t)sizeof(float)); }
+
 hipError_t launch_norm_bwd(const NormParams& P, hipStream_t stream) {
-  const int pieces = P.D / 8;
-  const int np = pieces > 1024 ? 2 : 1;
-  const int threads = ((pieces + np - 1) / np + 63) / 64 * 64;
-  const int groups = (int)(P.T < kGroups ? P.T : kGroups);
-  const int mode = !P.block ? 0 : P.post_weight ? 2 : 1;
+  const int groups = (int)bwd_groups(P.T, P.D), threads = bwd_threads(P.D);
   const auto go = [&](auto fs, auto fw, auto b) {
     constexpr int FS = decltype(fs)::value, FW = decltype(fw)::value, B = decltype(b)::value;
     const dim3 grid((unsigned)groups), block((unsigned)threads);
-    if (np == 1) launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B>, grid, block, stream, P);
+    if (P.D <= 8192) launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B>, grid, block, stream, P);
     else launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 2, B>, grid, block, stream, P);
     if (P.dweight) {
       const dim3 sums((unsigned)(P.D / 64), P.dgate || P.dpost_weight ? 2 : 1);
       launch(KID_NORM_SUM, k_norm_sum<FW>, sums, dim3(256), stream, P, groups);
     }
   };
-  const std::integral_constant<int, kWeightF32> f32;
-  const std::integral_constant<int, kWeightBf16> b16;
-  const auto by_weights = [&](auto b) {
+  const auto by_formats = [&](auto b) {
+    const Int<kWeightF32> f32;
+    const Int<kWeightBf16> b16;
     if (P.stream == kWeightF32) P.weights == kWeightF32 ? go(f32, f32, b) : go(f32, b16, b);
     else P.weights == kWeightF32 ? go(b16, f32, b) : go(b16, b16, b);
   };
-  if (mode == 0) by_weights(std::integral_constant<int, 0>());
-  else if (mode == 1) by_weights(std::integral_constant<int, 1>());
-  else by_weights(std::integral_constant<int, 2>());
+  if (!P.block) by_formats(Int<kNoBlock>());
+  else if (P.post_weight) by_formats(Int<kNormedBlock>());
+  else if (P.dgate) by_formats(Int<kGatedBlock>());
+  else by_formats(Int<kPlainBlock>());
   return hipGetLastError();
 }
 

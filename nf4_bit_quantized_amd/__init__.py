@@ -961,6 +961,12 @@ def qlora_checkpoint_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> i
 # The two ends of the layers: residual norm, log probabilities, distillation
 # ---------------------------------------------------------------------------
 
+def _rows(T: int, n: int, dtype, device):
+    """An uninitialised [T][n] tensor (empty_strided: 1.3 us of host time against 1.65 of empty with these arguments)."""
+    import torch
+    return torch.empty_strided((T, n), (n, 1), dtype=dtype, device=device)
+
+
 def _format(t, name: str, f16: bool = False) -> int:
     import torch
     dt = t.dtype
@@ -1020,13 +1026,13 @@ def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: fl
         if block is not None and h_out is None:
             h_out = torch.empty_like(h)
         if wide and X is None:
-            X = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+            X = _rows(T, D, torch.bfloat16, device)
         if narrow and codes is None:
-            codes = torch.empty((T, D), dtype=torch.uint8, device=device)
+            codes = _rows(T, D, torch.uint8, device)
         if narrow and scales is None:
-            scales = torch.empty(shape_s, dtype=torch.uint8, device=device)
+            scales = _rows(T, shape_s[1], torch.uint8, device)
         if stats is None:
-            stats = torch.empty((T, 2), dtype=torch.float32, device=device)
+            stats = _rows(T, 2, torch.float32, device)
         _check(lib().qlora_norm_fwd(T, D, _ptr(h), fs, _ptr(block), _ptr(weight), _ptr(post_weight), _ptr(gate), fw,
                                     float(scale), float(eps), _ptr(h_out), _ptr(X), _ptr(codes), _ptr(scales),
                                     _ptr(stats), st), name)
@@ -1130,15 +1136,15 @@ def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, w
     device = _one_device(name, logits, tokens, logprob, stats, entropy, top_ids, top_logprob)
     with _LaunchOn(device, stream, name) as st:
         if tokens is not None and logprob is None:
-            logprob = torch.empty(tokens.shape, dtype=torch.float32, device=device)
+            logprob = torch.empty_strided(tokens.shape, tokens.stride(), dtype=torch.float32, device=device)
         if stats is None:
-            stats = torch.empty((T, 2), dtype=torch.float32, device=device)
+            stats = _rows(T, 2, torch.float32, device)
         if want_entropy and entropy is None:
-            entropy = torch.empty((T,), dtype=torch.float32, device=device)
+            entropy = torch.empty_strided((T,), (1,), dtype=torch.float32, device=device)
         if top > 0 and top_ids is None:
-            top_ids = torch.empty((T, top), dtype=torch.int64, device=device)
+            top_ids = _rows(T, top, torch.int64, device)
         if top > 0 and top_logprob is None:
-            top_logprob = torch.empty((T, top), dtype=torch.float32, device=device)
+            top_logprob = _rows(T, top, torch.float32, device)
         _check(lib().qlora_token_logprob(T, vocab, _ptr(logits), fmt, ld, float(scale), n, _ptr(tokens), _ptr(logprob),
                                          _ptr(stats), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprob), st), name)
     return logprob, stats, entropy, top_ids, top_logprob
@@ -1175,7 +1181,7 @@ def qlora_token_logprob_bwd(logits, tokens, stats, d_logprob, scale: float = 1.0
     device = _one_device(name, logits, tokens, stats, d_logprob, entropy, d_entropy, dlogits)
     with _LaunchOn(device, stream, name) as st:
         if dlogits is None:
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+            dlogits = _rows(T, logits.shape[1], logits.dtype, device)
         _check(lib().qlora_token_logprob_bwd(T, vocab, _ptr(logits), fmt, ld, float(scale), n, _ptr(tokens),
                                              _ptr(stats), _ptr(entropy), _ptr(d_logprob), _ptr(d_entropy),
                                              _ptr(dlogits), logits.shape[1], _gradient_rows(name, logits, dlogits),
@@ -1208,9 +1214,9 @@ def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = Fals
     device = _one_device(name, logits, ids, values, loss, stats)
     with _LaunchOn(device, stream, name) as st:
         if loss is None:
-            loss = torch.empty((T,), dtype=torch.float32, device=device)
+            loss = torch.empty_strided((T,), (1,), dtype=torch.float32, device=device)
         if stats is None:
-            stats = torch.empty((T, 4), dtype=torch.float32, device=device)
+            stats = _rows(T, 4, torch.float32, device)
         _check(lib().qlora_distill_fwd(T, vocab, _ptr(logits), fmt, ld, float(scale), k, _ptr(ids), _ptr(values),
                                        1 if rest else 0, _ptr(loss), _ptr(stats), st), name)
     return loss, stats
@@ -1229,7 +1235,7 @@ def qlora_distill_bwd(logits, ids, values, stats, d_loss, scale: float = 1.0, re
     device = _one_device(name, logits, ids, values, stats, d_loss, dlogits)
     with _LaunchOn(device, stream, name) as st:
         if dlogits is None:
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+            dlogits = _rows(T, logits.shape[1], logits.dtype, device)
         _check(lib().qlora_distill_bwd(T, vocab, _ptr(logits), fmt, ld, float(scale), k, _ptr(ids), _ptr(values),
                                        1 if rest else 0, _ptr(stats), _ptr(d_loss), _ptr(dlogits), logits.shape[1],
                                        _gradient_rows(name, logits, dlogits), st), name)

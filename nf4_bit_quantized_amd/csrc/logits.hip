@@ -35,8 +35,9 @@ struct Sums {
   float m = -kMost, R = -kFar, s = 0.0f, t = 0.0f;
 };
 
+// Adds N elements; returns the largest of them.
 template <int N, bool ENT>
-__device__ __forceinline__ void add(Sums& a, const float (&f)[N], float c) {
+__device__ __forceinline__ float add(Sums& a, const float (&f)[N], float c) {
   float g = f[0];
 #pragma unroll
   for (int e = 1; e < N; ++e) g = fmaxf(g, f[e]);
@@ -54,6 +55,7 @@ __device__ __forceinline__ void add(Sums& a, const float (&f)[N], float c) {
     a.s += x;
     if constexpr (ENT) a.t = __builtin_fmaf(x, fmaxf(d, -kFar), a.t);  // 0 * -inf stays 0
   }
+  return g;
 }
 
 // The tokens of a teacher's list: bit b of byte p - first stands for element b
@@ -61,11 +63,19 @@ __device__ __forceinline__ void add(Sums& a, const float (&f)[N], float c) {
 constexpr int kWindow = 8192;
 
 // U pieces to a thread at a time, all loads of a round before the first use;
-// the last round loads no further than the row.
+// the last round loads no further than the row.  seen (or null) receives the
+// largest of every span of rounds.
 template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
-__device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first) {
+__device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first,
+                                      TopSeen<THREADS>* seen) {
   constexpr int E = kPer<F>, N = U < 4 ? U : 4;
+  const Spans spans = seen ? top_spans<THREADS, U>(p0, p1) : Spans{0, 1};
+  const int shift = spans.shift;
+  const bool note = spans.count > 1;
+  int rounds = 0;
+  float span = kNone;
   const auto round = [&](int p, auto all) {
+    if ((rounds & ((1 << shift) - 1)) == 0) span = kNone;
     u32x4_t w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -84,12 +94,16 @@ __device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1
           for (int e = 0; e < E; ++e) f[u * E + e] = (b >> e) & 1u ? kNone : f[u * E + e];
         }
       }
-      add<N * E, ENT>(a, f, c);
+      span = fmaxf(span, add<N * E, ENT>(a, f, c));
     }
+    if (note) seen->key[rounds >> shift][threadIdx.x] = (uint16_t)(ordered(span) >> 16);
+    ++rounds;
   };
   int p = p0 + (int)threadIdx.x;
   for (; p + (U - 1) * THREADS < p1; p += U * THREADS) round(p, std::true_type());
   if (p < p1) round(p, std::false_type());
+  if (note)
+    for (int left = (rounds + (1 << shift) - 1) >> shift; left < spans.count; ++left) seen->key[left][threadIdx.x] = 0;
 }
 
 struct Reduced {
@@ -136,7 +150,8 @@ __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double&
 // ids (LDS) are left out.
 template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
 __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
-                            uint32_t* mask, Reduced& sh, float* most = nullptr) {
+                            uint32_t* mask, Reduced& sh, float* most = nullptr,
+                            TopSeen<THREADS>* seen = nullptr) {
   constexpr int E = kPer<F>;
   const auto listed = [&](int64_t i) {
     bool hit = false;
@@ -163,7 +178,7 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
     }
   };
   Sums a;
-  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U, PAST>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0); });
+  pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U, PAST>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0, seen); });
   const int mine = edges && (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
   const float z_edge = mine >= 0 && !listed(mine) ? row.at(mine) : kNone;
   {
@@ -214,7 +229,8 @@ __device__ __forceinline__ float log_q(float z, float M, double scale, double lo
 template <int F, bool ENT, int THREADS, int U, bool PAST>
 __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   __shared__ Reduced red;
-  __shared__ TopShared sh_top;
+  __shared__ TopShared<THREADS> sh_top;
+  __shared__ TopSeen<THREADS> seen;
   const int64_t t = blockIdx.x;
   const Row<F> row(P.in.z, t, P.in.ld, (int)P.in.vocab);
   // the given tokens' logits come with the row's first pieces, not behind its last
@@ -223,7 +239,7 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   const bool given = id >= 0 && id < P.in.vocab;
   const float z = given ? row.at(id) : 0.0f;
   float most;
-  const Stats r = statistics<F, ENT, false, THREADS, U, PAST>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most);
+  const Stats r = statistics<F, ENT, false, THREADS, U, PAST>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most, P.top ? &seen : nullptr);
   const double log_s = log(r.S), scale = (double)P.in.scale;
   if (mine < P.n) P.logprob[t * P.n + mine] = given ? log_q(z, r.M, scale, log_s) : 0.0f;
   if (threadIdx.x == 0) {
@@ -232,7 +248,7 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
     if constexpr (ENT) P.entropy[t] = r.S == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (r.T / r.S));
   }
   if (P.top > 0) {
-    top_candidates<F, THREADS>(row, row.full0, row.full1, true, P.top, most, sh_top);
+    top_candidates<F, THREADS, U>(row, row.full0, row.full1, true, P.top, most, seen, sh_top);
     top_ranked<THREADS>(sh_top.key, sh_top.count, P.top, [&](int rank, uint64_t key) {
       P.top_ids[t * P.top + rank] = top_index(key);
       P.top_logprob[t * P.top + rank] = log_q(top_value(key), r.M, scale, log_s);
@@ -374,10 +390,10 @@ void by_format(int format, const Go& go) {
   else go(std::integral_constant<int, kWeightF16>());
 }
 
-// Alternatives read pieces of the row a second time, from the caches.
 // 4096 x 128256 bf16 (1.05 GB) after their gradients were written: 154 us past
-// the caches, 174 through them; 2048 x 128256 with 64 alternatives 115 and 112.
-bool read_past(const LogitsRows& in, int top) { return top == 0 && in.T * in.bytes() >= kCacheBytes; }
+// the caches, 174 through them; 2048 x 128256 80 and 86, with 64 alternatives
+// (which read some pieces twice) 94 and 98.
+bool read_past(const LogitsRows& in) { return in.T * in.bytes() >= kCacheBytes; }
 
 }  // namespace
 
@@ -401,7 +417,7 @@ hipError_t launch_score(const ScoreParams& P, hipStream_t stream) {
       else if (threads == 512) go(Int<512>(), past);
       else go(Int<1024>(), past);
     };
-    if (read_past(P.in, P.top)) by_threads(std::true_type());
+    if (read_past(P.in)) by_threads(std::true_type());
     else by_threads(std::false_type());
   });
   return hipGetLastError();
@@ -434,7 +450,7 @@ hipError_t launch_distill(const DistillParams& P, hipStream_t stream) {
         go(std::false_type(), Int<1024>(), Int<4>(), past);
       }
     };
-    if (read_past(P.in, 0)) by_threads(std::true_type());
+    if (read_past(P.in)) by_threads(std::true_type());
     else by_threads(std::false_type());
   });
   return hipGetLastError();

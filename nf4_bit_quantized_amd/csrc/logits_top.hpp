@@ -18,13 +18,35 @@ __device__ __forceinline__ uint64_t top_key(float v, int64_t i) {
 __device__ __forceinline__ int64_t top_index(uint64_t key) { return (int64_t)(0xFFFFFFFFu - (uint32_t)key); }
 __device__ __forceinline__ float top_value(uint64_t key) { return from_ordered((uint32_t)(key >> 32)); }
 
+// What a thread has seen of a row, in kSpans spans of 2^shift rounds of U pieces:
+// the first 16 bits of the key of each span's largest element.
+constexpr int kSpans = 8;
+template <int THREADS>
+struct TopSeen {
+  uint16_t key[kSpans][THREADS];
+};
+
+template <int THREADS>
 struct TopShared {
   uint64_t key[kCandidates];
-  uint32_t most[256];          // keys of the groups of threads
-  uint16_t who[1024];          // threads that hold candidates
+  uint32_t most[256];               // keys of the groups of threads
+  uint16_t who[kSpans * THREADS];   // threads, and their spans from bit 10 on, that hold candidates
   int count, holders;
   uint32_t low;
 };
+
+// One round is one span, and that the thread's `most`.
+struct Spans {
+  int shift, count;
+};
+template <int THREADS, int U>
+__device__ __forceinline__ Spans top_spans(int p0, int p1) {
+  const int rounds = (p1 - p0 + U * THREADS - 1) / (U * THREADS);
+  if (rounds <= 1) return Spans{0, 1};
+  int shift = 0;
+  while ((rounds - 1) >> shift >= kSpans) ++shift;
+  return Spans{shift, ((rounds - 1) >> shift) + 1};
+}
 
 // A limit that at least K of the wave's 64 * N keys reach: exactly K, or the
 // K-th largest with its last 32 - bits bits cleared; 0 if it has fewer than K
@@ -66,7 +88,7 @@ __device__ __forceinline__ void each_element(const Row<F>& row, int p0, int p1, 
 // above it): one pass over the pieces for each step.
 template <int F, int THREADS>
 __device__ void top_bisect(const Row<F>& row, int p0, int p1, bool edges, int K, uint64_t low, uint64_t high,
-                           TopShared& sh) {
+                           TopShared<THREADS>& sh) {
   while (low < high) {
     const uint64_t mid = low + ((high - low) >> 1) + 1;
     __syncthreads();
@@ -97,15 +119,19 @@ __device__ void top_bisect(const Row<F>& row, int p0, int p1, bool edges, int K,
   __syncthreads();
 }
 
-// The same with a pass over few pieces: `most` is the largest element of the
-// pieces p0 + threadIdx.x + j * THREADS (and of an edge) that this thread has
-// read, never above it and at least -kMost.  Of 256 groups of threads, K have
-// their largest element at or above the limit; so K elements are, and whatever
-// is lies with a thread whose `most` is: those threads' pieces alone are read
-// again.  Of 128256 logits by 512 threads, about K of 512 in the mean, all at
-// once.  Rows of many like elements overflow the candidates and are bisected.
-template <int F, int THREADS>
-__device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, int K, float most, TopShared& sh) {
+// The same with a pass over few pieces: `most` is the largest element that this
+// thread has read of the pieces p0 + threadIdx.x + j * THREADS (and of an edge),
+// never above it and at least -kMost.  Of 256 groups of threads, K have their
+// largest element at or above the limit; so K elements are, and whatever is lies
+// in a thread's span whose largest is: those spans alone are read again.  They
+// come from HBM, a line of 128 bytes for each piece of 16, so what counts is how
+// few.  Of 2048 x 128256 logits the 64 largest of each row take 95 us (80 without
+// them, 112 where all of a thread's pieces are read again), 20 take 88; of 4096
+// x 32000, 67 (47, 69) and 57.
+// Rows of many like elements overflow the candidates and are bisected.
+template <int F, int THREADS, int U>
+__device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, int K, float most,
+                               const TopSeen<THREADS>& seen, TopShared<THREADS>& sh) {
   constexpr int G = THREADS / 256;
   const uint32_t mine = most > -kMost ? ordered(most) : 0u;
   uint32_t group = mine;
@@ -130,7 +156,18 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
   }
   __syncthreads();
   const uint32_t low = sh.low;
-  if (mine >= low) sh.who[atomicAdd(&sh.holders, 1)] = (uint16_t)threadIdx.x;
+  const Spans spans = top_spans<THREADS, U>(p0, p1);
+  if (mine >= low) {
+    uint32_t held = 1;  // a bit for each span
+    if (spans.count > 1) {
+      held = 0;
+#pragma unroll
+      for (int span = 0; span < kSpans; ++span) held |= seen.key[span][threadIdx.x] >= low >> 16 ? 1u << span : 0u;
+      held &= (1u << spans.count) - 1;
+    }
+    int at = atomicAdd(&sh.holders, __popc(held));
+    for (; held; held &= held - 1) sh.who[at++] = (uint16_t)(threadIdx.x | (__ffs(held) - 1) << 10);
+  }
   __syncthreads();
   const auto offer = [&](float v, int64_t i) {
     const uint32_t k = ordered(v);
@@ -138,10 +175,12 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
     const int at = atomicAdd(&sh.count, 1);
     if (at < kCandidates) sh.key[at] = ((uint64_t)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
   };
-  const int holders = sh.holders, each = (p1 - p0 + THREADS - 1) / THREADS;
+  const int holders = sh.holders, each = U << spans.shift;
   for (int x = (int)threadIdx.x; x < holders * each; x += THREADS) {
-    const int j = x / holders, p = p0 + (int)sh.who[x - j * holders] + j * THREADS;
-    if (p >= p1) continue;
+    const int j = x / holders, who = (int)sh.who[x - j * holders];
+    const int64_t at = (int64_t)p0 + (who & 1023) + ((int64_t)(who >> 10) * each + j) * THREADS;
+    if (at >= p1) continue;
+    const int p = (int)at;
     float f[kPer<F>];
     unpack<F>(row.load(p), f);
     const int64_t i0 = (int64_t)p * kPer<F> - row.head;

@@ -577,7 +577,7 @@ int qlora_token_logprob(int64_t T, int64_t vocab, const void* logits, int32_t fo
  * logits themselves, with the same row stride; otherwise the two must not
  * overlap.  A row whose weights are all 0, and one of -inf alone, has gradient
  * 0 whatever its logits hold.  The top alternatives carry no gradient.
- * T * ceil(out_cols / 4096) < 2^24 is always enough (SHAPE otherwise).
+ * T * (out_cols / 4096 + 2) < 2^24 is always enough (SHAPE beyond the launch).
  */
 int qlora_token_logprob_bwd(int64_t T, int64_t vocab, const void* logits, int32_t format, int64_t ld, float scale,
                             int32_t n, const int64_t* tokens, const float* stats, const float* entropy,

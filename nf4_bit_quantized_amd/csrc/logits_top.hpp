@@ -5,6 +5,8 @@
 // in one order whatever the ties.
 #pragma once
 
+#include <type_traits>
+
 #include "logits.hpp"
 
 namespace qlora {
@@ -32,7 +34,7 @@ struct TopShared {
   uint32_t most[256];               // keys of the groups of threads
   uint16_t who[kSpans * THREADS];   // threads, and their spans from bit 10 on, that hold candidates
   int count, holders;
-  uint32_t low;
+  uint32_t low, below, above;
 };
 
 // One round is one span, and that the thread's `most`.
@@ -82,40 +84,91 @@ __device__ __forceinline__ void each_element(const Row<F>& row, int p0, int p1, 
   }
 }
 
-// Puts the elements of the pieces (and edges) with the K largest keys, and at
-// most kCandidates in all, into sh.key; sh.count is their number.  Bisects on
-// the key between `low` (at least K elements reach it) and `high` (none is
-// above it): one pass over the pieces for each step.
+// Puts the K largest elements of the pieces (and edges) into sh.key, whatever
+// their ties; `low` is at most the first 32 bits of the K-th largest's key.
+// First the K-th largest value: how many are above a value between the bounds
+// says on which side of it the K-th is, and the nearest elements on both sides
+// of it are the new bounds, so a row of few values is decided in as many passes
+// and any row in 32.  Then all above it, and as many equal to it as are left,
+// in the order of their indexes.
 template <int F, int THREADS>
-__device__ void top_bisect(const Row<F>& row, int p0, int p1, bool edges, int K, uint64_t low, uint64_t high,
-                           TopShared<THREADS>& sh) {
+__device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, uint32_t low, TopShared<THREADS>& sh) {
+  uint32_t high = 0xFFFFFFFFu, mid = low | 0xFFFFu;
   while (low < high) {
-    const uint64_t mid = low + ((high - low) >> 1) + 1;
     __syncthreads();
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    int mine = 0;
-    each_element<F, THREADS>(row, p0, p1, edges, [&](float v, int64_t i) { mine += top_key(v, i) >= mid ? 1 : 0; });
-    if (mine) atomicAdd(&sh.count, mine);
-    __syncthreads();
-    const int n = sh.count;
-    if (n >= K) {
-      low = mid;
-      if (n <= kCandidates) break;
-    } else {
-      high = mid - 1;
+    if (threadIdx.x == 0) {
+      sh.count = 0;
+      sh.below = 0u;
+      sh.above = 0xFFFFFFFFu;
     }
+    __syncthreads();
+    int n = 0;
+    uint32_t below = 0u, above = 0xFFFFFFFFu;
+    each_element<F, THREADS>(row, p0, p1, edges, [&](float v, int64_t) {
+      const uint32_t k = ordered(v);
+      if (k > mid) {
+        ++n;
+        above = k < above ? k : above;
+      } else {
+        below = k > below ? k : below;
+      }
+    });
+    if (n) atomicAdd(&sh.count, n);
+    atomicMax(&sh.below, below);
+    atomicMin(&sh.above, above);
+    __syncthreads();
+    if (sh.count >= K) low = sh.above;
+    else high = sh.below > low ? sh.below : low;
+    mid = low + (high - low) / 2;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   each_element<F, THREADS>(row, p0, p1, edges, [&](float v, int64_t i) {
-    const uint64_t key = top_key(v, i);
-    if (key >= low) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kCandidates) sh.key[at] = key;
-    }
+    if (ordered(v) > low) sh.key[atomicAdd(&sh.count, 1)] = top_key(v, i);  // fewer than K
   });
+  __syncthreads();
+  int left = K - sh.count;
+  // one step along the row: a thread's N elements from index i0 on, of which those in [0, vocab) count
+  const auto step = [&](auto size, const float* f, int64_t i0, bool in) {
+    constexpr int N = decltype(size)::value;
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) mine += in && ordered(f[e]) == low ? 1 : 0;
+    int before = mine;  // of this wave's lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int x = __shfl_up(before, o, 64);
+      if ((int)(threadIdx.x & 63) >= o) before += x;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63) sh.most[threadIdx.x >> 6] = (uint32_t)before;
+    __syncthreads();
+    before -= mine;
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+      if (w < (int)(threadIdx.x >> 6)) before += (int)sh.most[w];
+      all += (int)sh.most[w];
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (in && ordered(f[e]) == low && before++ < left) sh.key[atomicAdd(&sh.count, 1)] = top_key(f[e], i0 + e);
+    left -= all;
+  };
+  const auto edge = [&](int q0, int q1) {
+    const int q = q0 + (int)threadIdx.x;
+    const float f[1] = {q < q1 ? row.at(row.edge(q)) : 0.0f};
+    step(std::integral_constant<int, 1>(), f, q < q1 ? row.edge(q) : 0, q < q1);
+  };
+  if (edges) edge(0, row.edge0());
+  for (int p = p0; p < p1 && left > 0; p += THREADS) {
+    const int mine = p + (int)threadIdx.x;
+    float f[kPer<F>];
+    unpack<F>(row.load(mine < p1 ? mine : p), f);
+    step(std::integral_constant<int, kPer<F>>(), f, (int64_t)mine * kPer<F> - row.head, mine < p1);
+  }
+  if (edges && left > 0) edge(row.edge0(), row.edges());
   __syncthreads();
 }
 
@@ -128,7 +181,7 @@ __device__ void top_bisect(const Row<F>& row, int p0, int p1, bool edges, int K,
 // few.  Of 2048 x 128256 logits the 64 largest of each row take 95 us (80 without
 // them, 112 where all of a thread's pieces are read again), 20 take 88; of 4096
 // x 32000, 67 (47, 69) and 57.
-// Rows of many like elements overflow the candidates and are bisected.
+// Rows of many like elements overflow the candidates and take the way above.
 template <int F, int THREADS, int U>
 __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, int K, float most,
                                const TopSeen<THREADS>& seen, TopShared<THREADS>& sh) {
@@ -179,7 +232,7 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
   for (int x = (int)threadIdx.x; x < holders * each; x += THREADS) {
     const int j = x / holders, who = (int)sh.who[x - j * holders];
     const int64_t at = (int64_t)p0 + (who & 1023) + ((int64_t)(who >> 10) * each + j) * THREADS;
-    if (at >= p1) continue;
+    if (at >= p1 || *(volatile int*)&sh.count > kCandidates) continue;
     const int p = (int)at;
     float f[kPer<F>];
     unpack<F>(row.load(p), f);
@@ -192,7 +245,7 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
     offer(row.at(i), (int64_t)i);
   }
   __syncthreads();
-  if (sh.count > kCandidates) top_bisect<F, THREADS>(row, p0, p1, edges, K, (uint64_t)low << 32, ~(uint64_t)0, sh);
+  if (sh.count > kCandidates) top_exact<F, THREADS>(row, p0, p1, edges, K, low, sh);
 }
 
 // Calls out(rank, key) for the K largest of n keys, rank 0 the largest.  They

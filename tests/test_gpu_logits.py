@@ -192,6 +192,18 @@ def test_score_gradient(T, V, dtype, cols, offset, n, entropy):
     assert torch.equal(wide[:, 3:cols + 3], got) and (wide[:, :3] == 9).all() and (wide[:, cols + 3:] == 9).all()
 
 
+def test_entropy_gradient_alone():
+    import nf4_bit_quantized_amd as q
+    import torch
+    z = _logits(3, 8192, "float32", seed=5)
+    _, stats, H, _, _ = q.qlora_token_logprob(z, want_entropy=True)
+    d_H = torch.tensor([1.0, 0.0, -2.0], device="cuda")
+    got = q.qlora_token_logprob_bwd(z, None, stats, None, entropy=H, d_entropy=d_H)
+    rows = [ol.score_gradient(_np(z)[t], 1.0, [], [], *_np(stats)[t], float(H[t]), float(d_H[t])) for t in range(3)]
+    _near(got, np.stack([w for w, _ in rows]), np.stack([m for _, m in rows]), "dlogits")
+    assert not got[1].any()
+
+
 DISTILL = [  # T, V, dtype, columns, offset, k, scale
     (1, 1, "float32", 1, 0, 1, 1.0), (3, 11, "bfloat16", 12, 1, 11, 1.0), (4, 1000, "float16", 1000, 0, 128, 0.5),
     (2, 32000, "bfloat16", 32064, 0, 64, 1.0), (70, 4096, "float32", 4099, 3, 16, 2.0),

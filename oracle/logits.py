@@ -55,12 +55,13 @@ def named(tokens, V):
 def score_gradient(z, scale, tokens, d, M, log_s, H=0.0, d_H=0.0):
     """(gradient, magnitude) of one row: d of each given token, d_H of the entropy."""
     V = len(z)
+    tokens, d = np.asarray(tokens, np.int64), np.asarray(d, np.float64)
     in_ = named(tokens, V)
     w = np.zeros(V)
-    np.add.at(w, np.asarray(tokens)[in_], np.asarray(d, np.float64)[in_])
-    A = np.asarray(d, np.float64)[in_].sum()
-    size = np.abs(np.asarray(d, np.float64)[in_]).sum()
-    if M == NONE or (not np.asarray(d)[in_].any() and d_H == 0):
+    np.add.at(w, tokens[in_], d[in_])
+    A = d[in_].sum()
+    size = np.abs(d[in_]).sum()
+    if M == NONE or (not d[in_].any() and d_H == 0):
         return np.zeros(V), np.zeros(V)
     lq = log_q(z, M, log_s, scale)
     q = np.exp(lq)

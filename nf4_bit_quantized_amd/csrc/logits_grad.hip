@@ -11,8 +11,8 @@
 // once and every gradient written once, in pieces of 16 bytes.  A workgroup
 // takes kGroupPieces pieces of one row.  Its entries with their logits are
 // picked out before the first gradient is stored, so the gradients may take the
-// logits' place; the thread that owns an entry's piece then writes its gradient
-// over the common one.
+// logits' place; behind a barrier their gradients are written over the common
+// ones, a thread to an entry.
 #include <type_traits>
 
 #include "logits.hpp"
@@ -26,13 +26,9 @@ using namespace logits;
 
 constexpr int kThreads = 256, kPieces = 4, kGroupPieces = kThreads * kPieces;
 
-struct Entry {
-  int64_t id;
-  float w, z;
-};
-
 struct Shared {
-  Entry entry[kLogitsMost];
+  int64_t id[kLogitsMost];  // the group's entries: token, logit, weight
+  float z[kLogitsMost], w[kLogitsMost];
   int count;
   float A, A_listed;
 };
@@ -110,7 +106,12 @@ __device__ void entries(const LogitsGradParams& P, int64_t t, const Row<F>& row,
   for (int h = 0; h < 2; ++h) {
     const bool mine = in[h] && id[h] >= i0 && id[h] < i1;
     const uint64_t who = __ballot(mine);
-    if (mine) sh.entry[n + __popcll(who & (((uint64_t)1 << lane) - 1))] = Entry{id[h], w[h], row.at(id[h])};
+    if (mine) {
+      const int at = n + __popcll(who & (((uint64_t)1 << lane) - 1));
+      sh.id[at] = id[h];
+      sh.w[at] = w[h];
+      sh.z[at] = row.at(id[h]);
+    }
     n += __popcll(who);
   }
   const bool idle = __ballot(w[0] != 0.0f || w[1] != 0.0f) == 0 && A == 0.0f && A_listed == 0.0f;
@@ -174,14 +175,14 @@ __global__ __launch_bounds__(kThreads) void k_logits_grad(LogitsGradParams P, in
         if (i0 + e >= 0 && i0 + e < P.out_cols) store_element<F>(to, i0 + e, f[e]);
     }
   }
-  if (none) return;
-  for (int j = 0; j < sh.count; ++j) {
-    const Entry x = sh.entry[j];
-    if ((int)((x.id + out.head) / E - p0) % kThreads != (int)threadIdx.x) continue;
-    float w = 0.0f;  // a token named twice has the weights of both
-    for (int i = 0; i < sh.count; ++i) w += sh.entry[i].id == x.id ? sh.entry[i].w : 0.0f;
-    store_element<F>(to, x.id, gradient(x.z, w, sh.A_listed));
-  }
+  if (none || sh.count <= 0) return;
+  __syncthreads();
+  const int mine = (int)threadIdx.x;
+  if (mine >= sh.count) return;
+  const int64_t id = sh.id[mine];
+  float w = 0.0f;  // a token named twice has the weights of both, and both write the same
+  for (int j = 0; j < sh.count; ++j) w += sh.id[j] == id ? sh.w[j] : 0.0f;
+  store_element<F>(to, id, gradient(sh.z[mine], w, sh.A_listed));
 }
 
 }  // namespace

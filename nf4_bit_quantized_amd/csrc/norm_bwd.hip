@@ -240,14 +240,14 @@ __global__ __launch_bounds__(256) void k_norm_sum(NormParams P, int groups) {
   }
 }
 
-// Threads of a workgroup, and workgroups: two to a CU up to 4096 channels, one
+// Threads of a workgroup, and workgroups: two to a CU up to 2048 channels, one
 // above, each with the same number of tokens or one less.  us of both kernels
-// with one, two and four to a CU: 8192 x 2048 normed 45 42 44; 4096 x 4096 36 33
-// 35; 8192 x 1024 (fp32, normed; two, four and eight) 36 37 39.  With one and
-// two, 4096 x 8192: 65 67.
+// with one and two to a CU: 8192 x 2048 normed 45 42; 4096 x 4096 35 35; 1333 x
+// 4096 (fp32, normed and gated) 25.5 26.9, 600 of them 17.8 19.9; 4096 x 8192 65
+// 67; 8192 x 1024 (fp32, normed) with two and four 36 37.
 int bwd_threads(int64_t D) { return (int)((D / 8 / (D > 8192 ? 2 : 1) + 63) / 64 * 64); }
 int64_t bwd_groups(int64_t T, int64_t D) {
-  const int64_t most = D <= 4096 ? 512 : 256, turns = (T + most - 1) / most;
+  const int64_t most = D <= 2048 ? 512 : 256, turns = (T + most - 1) / most;
   return turns ? (T + turns - 1) / turns : 0;
 }
 

@@ -9,8 +9,8 @@
 //
 // A workgroup owns a token: every thread keeps its channels in registers
 // through both sums, so h and block are read once and h' and x written once.
-// Bound by HBM: 4096 x 8192 bf16 (268 MB) in 42.5 us, to the 8-bit form (235 MB)
-// in 38.2: 6.2 to 6.3 TB/s; one token 5 us.
+// Bound by HBM: 4096 x 8192 bf16 (268 MB) in 43 us, to the 8-bit form (235 MB)
+// in 40, 6 TB/s; one token 2.7 us of a call's 11.
 #include <type_traits>
 
 #include "fp8_form.hpp"
@@ -46,7 +46,7 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
 }
 
 // NP: pieces of eight channels a thread holds
-template <int FS, int FW, int NP>
+template <int FS, int FW, int NP, bool PAST>
 __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
   __shared__ float slot[2][16];
   const int64_t base = (int64_t)blockIdx.x * P.D;
@@ -63,8 +63,8 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
       b.zero();
       h[u].zero();
       if (p < pieces) {
-        b.load(P.block, base + 8 * p);
-        h[u].load(P.h, base + 8 * p);
+        b.template load<PAST>(P.block, base + 8 * p);
+        h[u].template load<PAST>(P.h, base + 8 * p);
       }
       b.values(g[u]);
 #pragma unroll
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
       h[u].values(v[u]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[u][e] = __builtin_fmaf(P.scale, g[u][e], v[u][e]);
-      if (p < pieces) store8<FS>(P.h_out, base + 8 * p, v[u]);
+      if (p < pieces) store8<FS, PAST>(P.h_out, base + 8 * p, v[u]);
     }
   } else {
 #pragma unroll
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
       const int p = u * step + (int)threadIdx.x;
       Eight<FS> h;
       h.zero();
-      if (p < pieces) h.load(P.h, base + 8 * p);
+      if (p < pieces) h.template load<PAST>(P.h, base + 8 * p);
       h.values(v[u]);
     }
   }
@@ -152,12 +152,18 @@ hipError_t launch_norm(const NormParams& P, hipStream_t stream) {
   // 4096 x 5120 normed and gated 34.6 30.9; 1333 x 4096 fp32 18.2 17.8; 256 x 4096 fp32 7.8 9.0.  Four are as fast as
   // two or slower (42.8, 39.6, 48.2, 32.3, 18.8).
   const int np = pieces > 1024 || (P.T > 512 && pieces >= 128) ? 2 : 1;
+  // tokens of 8192 bf16 channels, us through and past the caches: 1024 11.4 13.7, 2048 23.9 24.3, 2560 32.7 28.8, 4096
+  // 48.7 43.1 (to the 8-bit form 44.6 39.7)
+  const int64_t wide = P.stream == kWeightF32 ? 4 : 2;
+  const bool past = P.T * P.D * ((P.block ? 2 * wide + 2 : wide) + (P.x ? 2 : 0) + (P.codes ? 1 : 0)) >= kPastBytes;
   const int threads = ((pieces + np - 1) / np + 63) / 64 * 64;
   const dim3 grid((unsigned)P.T), block((unsigned)threads);
   const auto go = [&](auto fs, auto fw) {
     constexpr int FS = decltype(fs)::value, FW = decltype(fw)::value;
-    if (np == 1) launch(KID_NORM, k_norm<FS, FW, 1>, grid, block, stream, P);
-    else launch(KID_NORM, k_norm<FS, FW, 2>, grid, block, stream, P);
+    if (np == 1) past ? launch(KID_NORM, k_norm<FS, FW, 1, true>, grid, block, stream, P)
+                      : launch(KID_NORM, k_norm<FS, FW, 1, false>, grid, block, stream, P);
+    else past ? launch(KID_NORM, k_norm<FS, FW, 2, true>, grid, block, stream, P)
+              : launch(KID_NORM, k_norm<FS, FW, 2, false>, grid, block, stream, P);
   };
   const std::integral_constant<int, kWeightF32> f32;
   const std::integral_constant<int, kWeightBf16> b16;

@@ -42,19 +42,37 @@ hipError_t launch_norm_bwd(const NormParams& p, hipStream_t stream);
 
 namespace norm {
 
+// A call that moves more than half of what the last-level cache holds (256 MB)
+// takes the stream and the block past it: what is left of them there when they
+// are read again is little, and takes the place of the next layer's input.
+constexpr int64_t kPastBytes = (int64_t)128 << 20;
+
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 // Eight consecutive elements: 16 bytes of bf16, 32 of fp32.
+// PAST: not kept in the caches.
+template <bool PAST>
+__device__ __forceinline__ u32x4_t load16(const u32x4_t* q) {
+  if constexpr (PAST) return __builtin_nontemporal_load(q);
+  return *q;
+}
+template <bool PAST>
+__device__ __forceinline__ void store16(u32x4_t* q, u32x4_t v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+
 template <int F>
 struct Eight {
   u32x4_t a, b;
+  template <bool PAST = false>
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     if constexpr (F == kWeightF32) {
       const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p) + i);
-      a = q[0];
-      b = q[1];
+      a = load16<PAST>(q);
+      b = load16<PAST>(q + 1);
     } else {
-      a = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
+      a = load16<PAST>(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i));
     }
   }
   __device__ __forceinline__ void zero() { a = b = u32x4_t{0u, 0u, 0u, 0u}; }
@@ -74,7 +92,7 @@ struct Eight {
   }
 };
 
-template <int F>
+template <int F, bool PAST = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
   if constexpr (F == kWeightF32) {
     u32x4_t* q = reinterpret_cast<u32x4_t*>(static_cast<float*>(p) + i);
@@ -84,11 +102,12 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) 
       a[e] = __builtin_bit_cast(uint32_t, f[e]);
       b[e] = __builtin_bit_cast(uint32_t, f[4 + e]);
     }
-    q[0] = a;
-    q[1] = b;
+    store16<PAST>(q, a);
+    store16<PAST>(q + 1, b);
   } else {
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i) =
-        u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    store16<PAST>(
+        reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i),
+        u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])});
   }
 }
 

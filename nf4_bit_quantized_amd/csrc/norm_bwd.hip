@@ -13,9 +13,9 @@
 // until the end, and the next token's pieces load while this one's are summed;
 // the workgroups' sums are then added in their order by a second kernel (no
 // atomics).  dx, h', dh' and block are read once, dh and dblock written once.
-// Bound by HBM: 4096 x 8192 bf16 (335 MB) in 60 + 4 us, 5.2 TB/s; with a norm
-// behind the block and a gate (403 MB) 78 + 5; 1333 x 4096 in fp32 with both (98
-// MB) 20 + 5.
+// Bound by HBM: 4096 x 8192 bf16 (335 MB) in 56 us with the second kernel's 4, 6.0
+// TB/s; with a norm behind the block and a gate (403 MB) 76; 1333 x 4096 in fp32
+// with both (98 MB) 26.
 #include <type_traits>
 
 #include "norm.hpp"
@@ -31,7 +31,7 @@ using namespace norm;
 // a gate's gradient, whose dblock is a multiple of dh.
 enum Block { kNoBlock, kPlainBlock, kGatedBlock, kNormedBlock };
 
-template <int FS, int B>
+template <int FS, int B, bool PAST>
 struct Token {
   Eight<kWeightBf16> dx, block;
   Eight<FS> h, later;
@@ -43,11 +43,11 @@ struct Token {
       block.zero();
       return;
     }
-    dx.load(P.dx, i);
-    h.load(P.h_out, i);
-    if (P.dh_out) later.load(P.dh_out, i);
+    dx.template load<PAST>(P.dx, i);
+    h.template load<PAST>(P.h_out, i);
+    if (P.dh_out) later.template load<PAST>(P.dh_out, i);
     else later.zero();
-    if constexpr (B >= kGatedBlock) block.load(P.block, i);
+    if constexpr (B >= kGatedBlock) block.template load<PAST>(P.block, i);
   }
 };
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void factors(const NormParams& P, int p, bool in, flo
 // NP: pieces of eight channels a thread holds.  With one, its factors stay in
 // registers and the next token's pieces are on their way; with two (more than
 // 8192 channels) there is no room for either.
-template <int FS, int FW, int NP, int B>
+template <int FS, int FW, int NP, int B, bool PAST>
 __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
   __shared__ float4 slot[2][16];  // by token in turn: the one before may still be read
   const int pieces = P.D / 8, step = (int)blockDim.x, tid = (int)threadIdx.x, waves = step >> 6;
@@ -92,9 +92,9 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
   float w[8], c[8];
   if constexpr (NP == 1) factors<FW, B>(P, tid, tid < pieces, w, c);
   const float inv = 1.0f / (float)P.D;
-  Token<FS, B> now[NP], next[NP];
+  Token<FS, B, PAST> now[NP], next[NP];
   float2 r_now = {}, r_next = {};
-  const auto load = [&](int64_t t, Token<FS, B>(&to)[NP], float2& r) {
+  const auto load = [&](int64_t t, Token<FS, B, PAST>(&to)[NP], float2& r) {
 #pragma unroll
     for (int u = 0; u < NP; ++u) to[u].load(P, t * P.D + 8 * (u * step + tid), u * step + tid < pieces);
     r = float2{P.stats[2 * t], P.stats[2 * t + 1]};
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
         dw[u][e] = __builtin_fmaf(dx[e], n[e], dw[u][e]);
         d[e] = __builtin_fmaf(r, __builtin_fmaf(-mean, n[e], dx[e] * w[e]), d[e]);
       }
-      if (in) store8<FS>(P.dh, t * P.D + 8 * p, d);
+      if (in) store8<FS, PAST>(P.dh, t * P.D + 8 * p, d);
       if constexpr (B > kNoBlock) {
         float m[8];
         if constexpr (B >= kGatedBlock) {
@@ -260,11 +260,18 @@ size_t norm_bwd_part_bytes(int64_t T, int64_t D) { return (size_t)(bwd_groups(T,
 
 hipError_t launch_norm_bwd(const NormParams& P, hipStream_t stream) {
   const int groups = (int)bwd_groups(P.T, P.D), threads = bwd_threads(P.D);
+  // us of both kernels through and past the caches (all that is read, and dh; dblock is the next call's operand): 1024 x
+  // 8192 bf16 19.1 20.4, 2048 of them 38.0 33.4, 4096 66.7 56.3, normed and gated 86.8 76.0; 1333 x 4096 fp32, normed
+  // and gated, 26.8 30.1
+  const int64_t wide = P.stream == kWeightF32 ? 4 : 2, reads_block = P.post_weight || P.dgate ? 2 : 0;
+  const bool past = P.T * P.D * (2 + (P.dh_out ? 3 : 2) * wide + (P.block ? 2 : 0) + reads_block) >= kPastBytes;
   const auto go = [&](auto fs, auto fw, auto b) {
     constexpr int FS = decltype(fs)::value, FW = decltype(fw)::value, B = decltype(b)::value;
     const dim3 grid((unsigned)groups), block((unsigned)threads);
-    if (P.D <= 8192) launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B>, grid, block, stream, P);
-    else launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 2, B>, grid, block, stream, P);
+    if (P.D <= 8192) past ? launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B, true>, grid, block, stream, P)
+                          : launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 1, B, false>, grid, block, stream, P);
+    else past ? launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 2, B, true>, grid, block, stream, P)
+              : launch(KID_NORM_BWD, k_norm_bwd<FS, FW, 2, B, false>, grid, block, stream, P);
     if (P.dweight) {
       const dim3 sums((unsigned)(P.D / 64), P.dgate || P.dpost_weight ? 2 : 1);
       launch(KID_NORM_SUM, k_norm_sum<FW>, sums, dim3(256), stream, P, groups);

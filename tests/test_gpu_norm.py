@@ -172,3 +172,33 @@ def test_not_finite_stays_in_its_token():
     X, _, _ = q.qlora_norm_fwd(**v)
     fine = [0, 1, 3, 5]
     assert torch.equal(X[fine], clean[fine]) and X[2].isnan().all() and X[4, 1].isnan()
+
+
+@pytest.mark.parametrize("T,D,stream,post", [(70000, 512, "bfloat16", False), (20000, 1024, "float32", True),
+                                             (9000, 8192, "bfloat16", True), (3000, 16384, "float32", True)])
+def test_calls_that_pass_the_caches(T, D, stream, post):
+    """A large call's tokens are the small call's, bit for bit."""
+    import nf4_bit_quantized_amd as q
+    import torch
+    say(f"norm past the caches T {T} D {D} {stream} post {post}")
+    v = _inputs(T, D, getattr(torch, stream), torch.float32, post, post, seed=6)
+    x, h, stats = q.qlora_norm_fwd(form="both", **v)
+    dX, later = x[0].clone(), h.clone()
+    rest = {k: t for k, t in v.items() if k != "h"}
+    g = q.qlora_norm_bwd(dX, h, stats=stats, dh_out=later, **rest)
+    for rows in (slice(0, 600), slice(T - 600, T)):
+        few = {k: t[rows].clone() if t.dim() == 2 else t for k, t in v.items()}
+        x2, h2, s2 = q.qlora_norm_fwd(form="both", **few)
+        assert all(torch.equal(a[rows], b) for a, b in zip(x, x2)) and torch.equal(h[rows], h2)
+        assert torch.equal(stats[rows], s2)
+        few.pop("h")
+        g2 = q.qlora_norm_bwd(dX[rows].clone(), h2, stats=s2, dh_out=later[rows].clone(), **few)
+        assert torch.equal(g[0][rows], g2[0]) and torch.equal(g[1][rows], g2[1])
+    # the sums over all tokens: of the stored h, in 64 bits, a block of tokens at a time
+    want, mag = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    for t in range(0, T, 5000):
+        term = dX[t:t + 5000].double() * h[t:t + 5000].double() * stats[t:t + 5000, :1].double()
+        want += term.sum(0)
+        mag += term.abs().sum(0)
+    # T / 256 + 32 steps of a sum, and three roundings of a term
+    assert ((g[2].double() - want).abs() <= (T / 256 + 40) * 2.0 ** -24 * mag + 2.0 ** -24 * want.abs()).all()

@@ -705,7 +705,7 @@ class _LaunchOn:
     def __init__(self, device, stream, name: str):
         import torch
         self._device = self._stream = None
-        if device.index != torch.cuda.current_device():
+        if device.index != torch._C._cuda_getDevice():      # there are tensors on a GPU, so it is initialised
             self._device = torch.cuda.device(device)
         if stream is None:
             # torch.cuda.current_stream(device).cuda_stream, without the Stream object (2 us of a call's 10)
@@ -980,16 +980,19 @@ def _norm_args(name: str, h, block, weight, post_weight, gate):
     import torch
     if h is None or h.dim() != 2 or not h.is_contiguous():
         raise ValueError(f"{name}: the stream must be a contiguous 2-D tensor")
-    T, D = h.shape
+    shape = h.shape
+    T, D = shape
     if weight is None:
         raise ValueError(f"{name}: weight is required")
+    _check_in(weight, (D,), weight.dtype, "weight")
     if block is not None:
-        _check_in(block, (T, D), torch.bfloat16, "block")
+        _check_in(block, shape, torch.bfloat16, "block")
+        if post_weight is not None:
+            _check_in(post_weight, (D,), weight.dtype, "post_weight")
+        if gate is not None:
+            _check_in(gate, (D,), weight.dtype, "gate")
     elif post_weight is not None or gate is not None:
         raise ValueError(f"{name}: post_weight and gate need a block")
-    for t, what in ((weight, "weight"), (post_weight, "post_weight"), (gate, "gate")):
-        if t is not None:
-            _check_in(t, (D,), weight.dtype, what)
     return T, D, _format(h, "the stream"), _format(weight, "weight")
 
 
@@ -1010,9 +1013,12 @@ def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: fl
         raise ValueError(f"{name}: an output that form={form!r} does not write")
     if block is None and h_out is not None:
         raise ValueError(f"{name}: h_out needs a block")
-    _check_out(h_out, (T, D), h.dtype, "h_out")
-    _check_out(X, (T, D), torch.bfloat16, "X")
-    _check_out(stats, (T, 2), torch.float32, "stats")
+    if h_out is not None:
+        _check_out(h_out, (T, D), h.dtype, "h_out")
+    if X is not None:
+        _check_out(X, (T, D), torch.bfloat16, "X")
+    if stats is not None:
+        _check_out(stats, (T, 2), torch.float32, "stats")
     if narrow:
         shape_s = _scales_shape(T, D, 1)
         _check_out(codes, (T, D), torch.uint8, "codes")
@@ -1036,6 +1042,7 @@ def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: fl
     return x, h if block is None else h_out, stats
 
 
+@functools.lru_cache(maxsize=256)      # the sizes decide it
 def qlora_norm_bwd_workspace_bytes(T: int, D: int) -> int:
     n = ctypes.c_size_t()
     _check(lib().qlora_norm_bwd_workspace_bytes(int(T), int(D), ctypes.byref(n)), "qlora_norm_bwd_workspace_bytes")

@@ -509,6 +509,7 @@ int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, 
  * the backward; r_b is 1 without a norm behind the block.
  * h_out may be h.  Otherwise outputs must not alias inputs.  Matrices and
  * vectors are 16-byte aligned, scales and stats 4-byte.
+ * With eps 0 a row of zeros has r = inf and x NaN.
  * Deterministic.  Errors: NULL (post_weight or gate without a block, too),
  * SHAPE, UNSUPPORTED (formats, alignment, eps negative or not finite, scale
  * not finite), HIP.
@@ -545,8 +546,8 @@ int qlora_norm_bwd(int64_t T, int64_t D, const uint16_t* dX, const void* h_out, 
  * Log probabilities under q = softmax(scale * z), z being the first `vocab`
  * elements of each row of logits: format QLORA_W_F32, QLORA_W_BF16 or
  * QLORA_W_F16, rows ld >= vocab elements apart (a head whose rows were filled
- * up to a multiple of 64), any alignment of whole elements.  scale > 0: the
- * reciprocal of a temperature.  T < 2^22 rows.
+ * up to a multiple of 64), any alignment of whole elements.  scale in
+ * (0, 2^100]: the reciprocal of a temperature.  T < 2^22 rows.
  *   stats   fp32 [T][2]: M = max z and log S, S = sum exp(scale (z - M)); the
  *           row's log-sum-exp is scale M + log S
  *   logprob fp32 [T][n]: log q of tokens [T][n], n <= 128; a token outside

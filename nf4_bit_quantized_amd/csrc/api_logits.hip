@@ -1,14 +1,15 @@
 // C entry points of the operators on logits: validation and launches.  The
 // declarations, with argument meaning and error behaviour, are in
 // include/qlora.h.
-#include <cmath>
-
 #include "api.hpp"
 #include "logits.hpp"
 
 using namespace qlora;
 
 namespace {
+
+// scale * log2(e) and its product with a difference of logits stay finite or go to -inf
+constexpr float kMostScale = 1.2676506e30f;  // 2^100
 
 int64_t format_bytes(int32_t format) { return format == QLORA_W_F32 ? 4 : 2; }
 bool aligned_to(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
@@ -17,7 +18,7 @@ int check_rows(int64_t T, int64_t vocab, int32_t format, int64_t ld, float scale
   if (format != QLORA_W_F32 && format != QLORA_W_BF16 && format != QLORA_W_F16) return QLORA_ERR_UNSUPPORTED;
   if (T < 0 || T > kLogitsMostRows || vocab <= 0 || vocab >= kMaxDim - 16 || ld < vocab || ld >= kMaxDim)
     return QLORA_ERR_SHAPE;
-  if (!(scale > 0.0f) || std::isinf(scale)) return QLORA_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || scale > kMostScale) return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
 }
 

@@ -62,7 +62,7 @@ def test_norm_backward_arguments():
 
 
 ROWS = [(0, -1, SHAPE), (0, 1 << 22, SHAPE), (1, 0, SHAPE), (1, 1 << 31, SHAPE), (4, 99, SHAPE), (4, 1 << 31, SHAPE),
-        (3, 3, UNSUP), (3, -1, UNSUP), (5, 0.0, UNSUP), (5, -1.0, UNSUP), (5, NAN, UNSUP), (5, INF, UNSUP),
+        (3, 3, UNSUP), (3, -1, UNSUP), (5, 0.0, UNSUP), (5, -1.0, UNSUP), (5, NAN, UNSUP), (5, INF, UNSUP), (5, 2.0 ** 101, UNSUP),
         (2, None, NULL), (2, F + 1, UNSUP)]
 
 

@@ -16,6 +16,8 @@ describe, step by step and in the pages' order:
 * ``oracle.bf16`` -- the oracle's own bfloat16 round-to-nearest-even.
 * ``oracle.fp8``  -- the 8-bit form and the layer over 8-bit operands.
 * ``oracle.optim`` -- the AdamW update of the adapter parameters.
+* ``oracle.norm``  -- the residual norm and its backward.
+* ``oracle.logits`` -- log probabilities, entropy, the largest logits, the distillation loss, and their gradients.
 
 Page keys used in citations (titles of the pages the method is read from):
 

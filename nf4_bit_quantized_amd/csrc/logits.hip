@@ -78,7 +78,7 @@ template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
 __device__ __forceinline__ void sweep(Sums& a, const Row<F>& row, int p0, int p1, float c, const uint8_t* mask, int first,
                                       TopSeen<THREADS>* seen) {
   constexpr int E = kPer<F>, N = U < 4 ? U : 4;
-  const Spans spans = seen ? top_spans<THREADS, U>(p0, p1) : Spans{0, 1};
+  const Spans spans = seen ? top_spans<THREADS, U>(p1 - p0) : Spans{0, 1};
   const int shift = spans.shift;
   const bool note = spans.count > 1;
   int rounds = 0;
@@ -120,7 +120,7 @@ struct Reduced {
   double s[16], t[16];
 };
 
-// What a row (or a part of one) comes to: M, S and T = sum e log2(e) with
+// What a row comes to: M, S and T = sum e log2(e) with
 // e = 2^(c (z - M)).
 struct Stats {
   float M;
@@ -154,11 +154,10 @@ __device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double&
   }
 }
 
-// The statistics of pieces p0 .. p1 - 1 and, with `edges`, of the elements
-// outside the full pieces; every thread gets them.  With MASK the k elements of
+// The statistics of the row; every thread gets them.  With MASK the k elements of
 // ids (LDS) are left out.
 template <int F, bool ENT, bool MASK, int THREADS, int U, bool PAST>
-__device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float c, const int64_t* ids, int k,
+__device__ Stats statistics(const Row<F>& row, float c, const int64_t* ids, int k,
                             uint32_t* mask, Reduced& sh, float* most = nullptr,
                             TopSeen<THREADS>* seen = nullptr) {
   constexpr int E = kPer<F>;
@@ -169,8 +168,9 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
     return hit;
   };
   const auto pass = [&](const auto& body) {
+    const int p0 = row.full0, p1 = row.full1;
     for (int q0 = p0; q0 < p1; q0 += MASK ? kWindow : p1 - p0) {
-      const int q1 = MASK && q0 + kWindow < p1 ? q0 + kWindow : p1;
+      const int q1 = MASK && p1 - q0 > kWindow ? q0 + kWindow : p1;
       if constexpr (MASK) {
         __syncthreads();
         for (int w = (int)threadIdx.x; w < kWindow / 4; w += THREADS) mask[w] = 0u;
@@ -189,7 +189,7 @@ __device__ Stats statistics(const Row<F>& row, int p0, int p1, bool edges, float
   };
   Sums a;
   pass([&](int q0, int q1) { sweep<F, ENT, MASK, THREADS, U, PAST>(a, row, q0, q1, c, reinterpret_cast<const uint8_t*>(mask), q0, seen); });
-  const int mine = edges && (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
+  const int mine = (int)threadIdx.x < row.edges() ? row.edge((int)threadIdx.x) : -1;
   const float z_edge = mine >= 0 && !listed(mine) ? row.at(mine) : kNone;
   {
     const float f[1] = {z_edge};
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
   const bool given = id >= 0 && id < P.in.vocab;
   const float z = given ? row.at(id) : 0.0f;
   float most;
-  const Stats r = statistics<F, ENT, false, THREADS, U, PAST>(row, row.full0, row.full1, true, c, nullptr, 0, nullptr, red, &most, P.top ? &seen : nullptr);
+  const Stats r = statistics<F, ENT, false, THREADS, U, PAST>(row, c, nullptr, 0, nullptr, red, &most, P.top ? &seen : nullptr);
   const double log_s = log(r.S), scale = (double)P.in.scale;
   if (mine < P.n) P.logprob[t * P.n + mine] = given ? log_q(z, r.M, scale, log_s) : 0.0f;
   if (threadIdx.x == 0) {
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
     if constexpr (ENT) P.entropy[t] = r.S == 0.0 ? 0.0f : (float)(log_s - 0.6931471805599453 * (r.T / r.S));
   }
   if (P.top > 0) {
-    top_candidates<F, THREADS, U>(row, row.full0, row.full1, true, P.top, most, seen, sh_top);
+    top_candidates<F, THREADS, U>(row, P.top, most, seen, sh_top);
     top_ranked<THREADS>(sh_top.key, sh_top.count, P.top, [&](int rank, uint64_t key) {
       P.top_ids[t * P.top + rank] = top_index(key);
       P.top_logprob[t * P.top + rank] = log_q(top_value(key), r.M, scale, log_s);
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(THREADS) void k_distill(DistillParams P, float c) {
     }
   }
   if constexpr (REST) __syncthreads();
-  const Stats r = statistics<F, false, REST, THREADS, U, PAST>(row, row.full0, row.full1, true, c, ids, P.k, mask, red);
+  const Stats r = statistics<F, false, REST, THREADS, U, PAST>(row, c, ids, P.k, mask, red);
   if (threadIdx.x < 64) distill_finish<REST>(P, t, list, ids, r);
 }
 

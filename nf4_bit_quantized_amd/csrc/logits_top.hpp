@@ -42,57 +42,54 @@ struct Spans {
   int shift, count;
 };
 template <int THREADS, int U>
-__device__ __forceinline__ Spans top_spans(int p0, int p1) {
-  const int rounds = (p1 - p0 + U * THREADS - 1) / (U * THREADS);
+__device__ __forceinline__ Spans top_spans(int pieces) {
+  const int rounds = (pieces + U * THREADS - 1) / (U * THREADS);
   if (rounds <= 1) return Spans{0, 1};
   int shift = 0;
   while ((rounds - 1) >> shift >= kSpans) ++shift;
   return Spans{shift, ((rounds - 1) >> shift) + 1};
 }
 
-// A limit that at least K of the wave's 64 * N keys reach: exactly K, or the
-// K-th largest with its last 32 - bits bits cleared; 0 if it has fewer than K
-// above 0.  Bit by bit from the top.
-template <int N>
-__device__ __forceinline__ uint32_t top_limit(const uint32_t (&key)[N], int K, int bits) {
+// A limit that at least K of the wave's 256 keys reach: exactly K, or the K-th
+// largest with its last 16 bits cleared; 0 if it has fewer than K above 0.  Bit
+// by bit from the top.
+__device__ __forceinline__ uint32_t top_limit(const uint32_t (&key)[4], int K) {
   uint32_t t = 0;
-  for (int b = 31; b >= 32 - bits; --b) {
+  for (int b = 31; b >= 16; --b) {
     const uint32_t next = t | (1u << b);
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) n += __popcll(__ballot(key[j] >= next));
+    for (int j = 0; j < 4; ++j) n += __popcll(__ballot(key[j] >= next));
     if (n >= K) t = next;
     if (n == K) break;
   }
   return t;
 }
 
-// Calls at(value, index) for the elements of pieces p0 .. p1 - 1 and, with
-// `edges`, for those outside the full pieces.
+// Calls at(value, index) for every element of the row.
 template <int F, int THREADS, class At>
-__device__ __forceinline__ void each_element(const Row<F>& row, int p0, int p1, bool edges, const At& at) {
-  for (int p = p0 + (int)threadIdx.x; p < p1; p += THREADS) {
+__device__ __forceinline__ void each_element(const Row<F>& row, const At& at) {
+  for (int p = row.full0 + (int)threadIdx.x; p < row.full1; p += THREADS) {
     float f[kPer<F>];
     unpack<F>(row.load(p), f);
     const int64_t i0 = (int64_t)p * kPer<F> - row.head;
 #pragma unroll
     for (int e = 0; e < kPer<F>; ++e) at(f[e], i0 + e);
   }
-  if (edges && (int)threadIdx.x < row.edges()) {
+  if ((int)threadIdx.x < row.edges()) {
     const int i = row.edge((int)threadIdx.x);
     at(row.at(i), (int64_t)i);
   }
 }
 
-// Puts the K largest elements of the pieces (and edges) into sh.key, whatever
-// their ties; `low` is at most the first 32 bits of the K-th largest's key.
+// Puts the K largest elements of the row into sh.key, whatever their ties; `low` is at most the first 32 bits of the K-th largest's key.
 // First the K-th largest value: how many are above a value between the bounds
 // says on which side of it the K-th is, and the nearest elements on both sides
 // of it are the new bounds, so a row of few values is decided in as many passes
 // and any row in 32.  Then all above it, and as many equal to it as are left,
 // in the order of their indexes.
 template <int F, int THREADS>
-__device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, uint32_t low, TopShared<THREADS>& sh) {
+__device__ void top_exact(const Row<F>& row, int K, uint32_t low, TopShared<THREADS>& sh) {
   uint32_t high = 0xFFFFFFFFu, mid = low | 0xFFFFu;
   while (low < high) {
     __syncthreads();
@@ -104,7 +101,7 @@ __device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, 
     __syncthreads();
     int n = 0;
     uint32_t below = 0u, above = 0xFFFFFFFFu;
-    each_element<F, THREADS>(row, p0, p1, edges, [&](float v, int64_t) {
+    each_element<F, THREADS>(row, [&](float v, int64_t) {
       const uint32_t k = ordered(v);
       if (k > mid) {
         ++n;
@@ -124,7 +121,7 @@ __device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, 
   __syncthreads();
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
-  each_element<F, THREADS>(row, p0, p1, edges, [&](float v, int64_t i) {
+  each_element<F, THREADS>(row, [&](float v, int64_t i) {
     if (ordered(v) > low) sh.key[atomicAdd(&sh.count, 1)] = top_key(v, i);  // fewer than K
   });
   __syncthreads();
@@ -161,19 +158,20 @@ __device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, 
     const float f[1] = {q < q1 ? row.at(row.edge(q)) : 0.0f};
     step(std::integral_constant<int, 1>(), f, q < q1 ? row.edge(q) : 0, q < q1);
   };
-  if (edges) edge(0, row.edge0());
-  for (int p = p0; p < p1 && left > 0; p += THREADS) {
+  edge(0, row.edge0());
+  for (int p = row.full0; p < row.full1 && left > 0; p += THREADS) {
     const int mine = p + (int)threadIdx.x;
+    const bool in = mine < row.full1;
     float f[kPer<F>];
-    unpack<F>(row.load(mine < p1 ? mine : p), f);
-    step(std::integral_constant<int, kPer<F>>(), f, (int64_t)mine * kPer<F> - row.head, mine < p1);
+    unpack<F>(row.load(in ? mine : p), f);
+    step(std::integral_constant<int, kPer<F>>(), f, (int64_t)mine * kPer<F> - row.head, in);
   }
-  if (edges && left > 0) edge(row.edge0(), row.edges());
+  if (left > 0) edge(row.edge0(), row.edges());
   __syncthreads();
 }
 
 // The same with a pass over few pieces: `most` is the largest element that this
-// thread has read of the pieces p0 + threadIdx.x + j * THREADS (and of an edge),
+// thread has read, of the full pieces every THREADS-th and at most one edge,
 // never above it and at least -kMost.  Of 256 groups of threads, K have their
 // largest element at or above the limit; so K elements are, and whatever is lies
 // in a thread's span whose largest is: those spans alone are read again.  They
@@ -183,8 +181,8 @@ __device__ void top_exact(const Row<F>& row, int p0, int p1, bool edges, int K, 
 // x 32000, 67 (47, 69) and 57.
 // Rows of many like elements overflow the candidates and take the way above.
 template <int F, int THREADS, int U>
-__device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, int K, float most,
-                               const TopSeen<THREADS>& seen, TopShared<THREADS>& sh) {
+__device__ void top_candidates(const Row<F>& row, int K, float most, const TopSeen<THREADS>& seen,
+                               TopShared<THREADS>& sh) {
   constexpr int G = THREADS / 256;
   const uint32_t mine = most > -kMost ? ordered(most) : 0u;
   uint32_t group = mine;
@@ -204,12 +202,12 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
 #pragma unroll
     for (int j = 0; j < 4; ++j) key[j] = sh.most[64 * j + threadIdx.x];
     // the type of the logits decides sixteen bits of a key; for fp32 it is a limit all the same
-    const uint32_t low = top_limit<4>(key, K, 16);
+    const uint32_t low = top_limit(key, K);
     if (threadIdx.x == 0) sh.low = low;
   }
   __syncthreads();
   const uint32_t low = sh.low;
-  const Spans spans = top_spans<THREADS, U>(p0, p1);
+  const Spans spans = top_spans<THREADS, U>(row.full1 - row.full0);
   if (mine >= low) {
     uint32_t held = 1;  // a bit for each span
     if (spans.count > 1) {
@@ -231,8 +229,8 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
   const int holders = sh.holders, each = U << spans.shift;
   for (int x = (int)threadIdx.x; x < holders * each; x += THREADS) {
     const int j = x / holders, who = (int)sh.who[x - j * holders];
-    const int64_t at = (int64_t)p0 + (who & 1023) + ((int64_t)(who >> 10) * each + j) * THREADS;
-    if (at >= p1 || *(volatile int*)&sh.count > kCandidates) continue;
+    const int64_t at = (int64_t)row.full0 + (who & 1023) + ((int64_t)(who >> 10) * each + j) * THREADS;
+    if (at >= row.full1 || *(volatile int*)&sh.count > kCandidates) continue;
     const int p = (int)at;
     float f[kPer<F>];
     unpack<F>(row.load(p), f);
@@ -240,12 +238,12 @@ __device__ void top_candidates(const Row<F>& row, int p0, int p1, bool edges, in
 #pragma unroll
     for (int e = 0; e < kPer<F>; ++e) offer(f[e], i0 + e);
   }
-  if (edges && (int)threadIdx.x < row.edges()) {
+  if ((int)threadIdx.x < row.edges()) {
     const int i = row.edge((int)threadIdx.x);
     offer(row.at(i), (int64_t)i);
   }
   __syncthreads();
-  if (sh.count > kCandidates) top_exact<F, THREADS>(row, p0, p1, edges, K, low, sh);
+  if (sh.count > kCandidates) top_exact<F, THREADS>(row, K, low, sh);
 }
 
 // Calls out(rank, key) for the K largest of n keys, rank 0 the largest.  They

@@ -1035,8 +1035,8 @@ def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: fl
             scales = torch.empty(shape_s, dtype=torch.uint8, device=device)
         if stats is None:
             stats = torch.empty_strided((T, 2), (2, 1), dtype=torch.float32, device=device)
-        _check(lib().qlora_norm_fwd(T, D, h.data_ptr(), fs, _ptr(block), weight.data_ptr(), _ptr(post_weight), _ptr(gate), fw,
-                                    float(scale), float(eps), _ptr(h_out), _ptr(X), _ptr(codes), _ptr(scales),
+        _check(lib().qlora_norm_fwd(T, D, h.data_ptr(), fs, _ptr(block), weight.data_ptr(),
+                                    _ptr(post_weight), _ptr(gate), fw, float(scale), float(eps), _ptr(h_out), _ptr(X), _ptr(codes), _ptr(scales),
                                     stats.data_ptr(), st), name)
     x = X if form == "bf16" else (codes, scales) if form == "fp8" else (X, codes, scales)
     return x, h if block is None else h_out, stats
@@ -1086,10 +1086,10 @@ def qlora_norm_bwd(dX, h_out, weight, stats, block=None, post_weight=None, gate=
                 for g, w, _ in grads)
             nbytes = qlora_norm_bwd_workspace_bytes(T, D)
         ws = _workspace(nbytes, device, workspace)
-        _check(lib().qlora_norm_bwd(T, D, dX.data_ptr(), h_out.data_ptr(), fs, _ptr(block), weight.data_ptr(), _ptr(post_weight),
-                                    _ptr(gate), fw, float(scale), stats.data_ptr(), _ptr(dh_out), dh.data_ptr(), _ptr(dblock),
-                                    _ptr(dweight), _ptr(dpost_weight), _ptr(dgate), 1 if accumulate else 0, _ptr(ws),
-                                    nbytes, st), name)
+        _check(lib().qlora_norm_bwd(T, D, dX.data_ptr(), h_out.data_ptr(), fs, _ptr(block), weight.data_ptr(),
+                                    _ptr(post_weight), _ptr(gate), fw, float(scale), stats.data_ptr(), _ptr(dh_out),
+                                    dh.data_ptr(), _ptr(dblock), _ptr(dweight), _ptr(dpost_weight), _ptr(dgate),
+                                    1 if accumulate else 0, _ptr(ws), nbytes, st), name)
     return dh, dblock, dweight, dpost_weight, dgate
 
 
@@ -1148,8 +1148,9 @@ def qlora_token_logprob(logits, tokens=None, scale: float = 1.0, top: int = 0, w
             top_ids = torch.empty_strided((T, top), (top, 1), dtype=torch.int64, device=device)
         if top > 0 and top_logprob is None:
             top_logprob = torch.empty_strided((T, top), (top, 1), dtype=torch.float32, device=device)
-        _check(lib().qlora_token_logprob(T, vocab, logits.data_ptr(), fmt, ld, float(scale), n, _ptr(tokens), _ptr(logprob),
-                                         stats.data_ptr(), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprob), st), name)
+        _check(lib().qlora_token_logprob(T, vocab, logits.data_ptr(), fmt, ld, float(scale), n, _ptr(tokens),
+                                         _ptr(logprob), stats.data_ptr(), _ptr(entropy), top, _ptr(top_ids),
+                                         _ptr(top_logprob), st), name)
     return logprob, stats, entropy, top_ids, top_logprob
 
 
@@ -1220,8 +1221,8 @@ def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = Fals
             loss = torch.empty_strided((T,), (1,), dtype=torch.float32, device=device)
         if stats is None:
             stats = torch.empty_strided((T, 4), (4, 1), dtype=torch.float32, device=device)
-        _check(lib().qlora_distill_fwd(T, vocab, logits.data_ptr(), fmt, ld, float(scale), k, ids.data_ptr(), values.data_ptr(),
-                                       1 if rest else 0, loss.data_ptr(), stats.data_ptr(), st), name)
+        _check(lib().qlora_distill_fwd(T, vocab, logits.data_ptr(), fmt, ld, float(scale), k, ids.data_ptr(),
+                                       values.data_ptr(), 1 if rest else 0, loss.data_ptr(), stats.data_ptr(), st), name)
     return loss, stats
 
 
@@ -1239,8 +1240,9 @@ def qlora_distill_bwd(logits, ids, values, stats, d_loss, scale: float = 1.0, re
     with _LaunchOn(device, stream, name) as st:
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=device)
-        _check(lib().qlora_distill_bwd(T, vocab, logits.data_ptr(), fmt, ld, float(scale), k, ids.data_ptr(), values.data_ptr(),
-                                       1 if rest else 0, stats.data_ptr(), d_loss.data_ptr(), dlogits.data_ptr(), logits.shape[1],
+        _check(lib().qlora_distill_bwd(T, vocab, logits.data_ptr(), fmt, ld, float(scale), k, ids.data_ptr(),
+                                       values.data_ptr(), 1 if rest else 0, stats.data_ptr(), d_loss.data_ptr(),
+                                       dlogits.data_ptr(), logits.shape[1],
                                        _gradient_rows(name, logits, dlogits), st), name)
     return dlogits
 

@@ -133,6 +133,44 @@ def test_side_stream_and_replays(kind):
         same(_step(q, (a, b)[1 - turn], stored, kind), want[1 - turn])      # eager work between the replays
 
 
+def test_given_stream_and_workspace():
+    """stream= enqueues there and allocates there; one workspace serves calls in turn, captured ones too."""
+    import nf4_bit_quantized_amd as q
+    import torch
+    say("given stream and workspace")
+    s = _step_inputs(seed=4)
+    side = torch.cuda.Stream()
+    x, h, stats = q.qlora_norm_fwd(s["h"], s["weight"], **_norm_args(s))
+    want = q.qlora_norm_bwd(x, h, s["weight"], stats, **_norm_args(s))
+    z = _logits(6, 3001, "float16", seed=8)
+    tokens = torch.arange(6, device="cuda")
+    ref = q.qlora_token_logprob(z, tokens, top=4)
+    ws = torch.empty(q.qlora_norm_bwd_workspace_bytes(*s["h"].shape), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    x2, h2, s2 = q.qlora_norm_fwd(s["h"], s["weight"], stream=side, **_norm_args(s))
+    got = q.qlora_norm_bwd(x2, h2, s["weight"], s2, workspace=ws, stream=side, **_norm_args(s))
+    out = q.qlora_token_logprob(z, tokens, top=4, stream=side)
+    loss = q.qlora_distill_fwd(z, out[3], out[4], stream=side)
+    d = q.qlora_distill_bwd(z, out[3], out[4], loss[1], torch.ones_like(loss[0]), stream=side)
+    side.synchronize()
+    assert torch.equal(x, x2) and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(out, ref) if a is not None) and d.isfinite().all()
+    graphs = []
+    for rows in (slice(0, 48), slice(0, 17)):
+        few = {k: v[rows].clone() if k in ("h", "block") else v for k, v in s.items()}
+        a = q.qlora_norm_fwd(few["h"], few["weight"], **_norm_args(few))
+        expect = q.qlora_norm_bwd(a[0], a[1], few["weight"], a[2], **_norm_args(few))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            r = q.qlora_norm_bwd(a[0], a[1], few["weight"], a[2], workspace=ws, **_norm_args(few))
+        graphs.append((graph, r, expect, a, few))
+    for turn in (0, 1, 1, 0):
+        graph, r, expect = graphs[turn][:3]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, expect))
+
+
 def test_scores_on_a_side_stream_and_replayed():
     import nf4_bit_quantized_amd as q
     import torch

@@ -1036,8 +1036,8 @@ def qlora_norm_fwd(h, weight, block=None, post_weight=None, gate=None, scale: fl
         if stats is None:
             stats = torch.empty_strided((T, 2), (2, 1), dtype=torch.float32, device=device)
         _check(lib().qlora_norm_fwd(T, D, h.data_ptr(), fs, _ptr(block), weight.data_ptr(),
-                                    _ptr(post_weight), _ptr(gate), fw, float(scale), float(eps), _ptr(h_out), _ptr(X), _ptr(codes), _ptr(scales),
-                                    stats.data_ptr(), st), name)
+                                    _ptr(post_weight), _ptr(gate), fw, float(scale), float(eps), _ptr(h_out),
+                                    _ptr(X), _ptr(codes), _ptr(scales), stats.data_ptr(), st), name)
     x = X if form == "bf16" else (codes, scales) if form == "fp8" else (X, codes, scales)
     return x, h if block is None else h_out, stats
 
@@ -1222,7 +1222,8 @@ def qlora_distill_fwd(logits, ids, values, scale: float = 1.0, rest: bool = Fals
         if stats is None:
             stats = torch.empty_strided((T, 4), (4, 1), dtype=torch.float32, device=device)
         _check(lib().qlora_distill_fwd(T, vocab, logits.data_ptr(), fmt, ld, float(scale), k, ids.data_ptr(),
-                                       values.data_ptr(), 1 if rest else 0, loss.data_ptr(), stats.data_ptr(), st), name)
+                                       values.data_ptr(), 1 if rest else 0, loss.data_ptr(), stats.data_ptr(), st),
+               name)
     return loss, stats
 
 

@@ -496,7 +496,7 @@ int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, 
  * 16384; T < 2^22):
  *   m  = block * r_b,  r_b = 1 / sqrt(mean(block^2) + eps)
  *   h' = h + scale * gate * post_weight * m
- *   x  = weight * h' * r,  r = 1 / sqrt(mean(h'^2) + eps)
+ *   x  = (h' * r) * weight,  r = 1 / sqrt(mean(h'^2) + eps)
  * block: a layer's output, bf16 [T][D]; NULL leaves h as it is (h_out is then
  * not written and may be NULL).  post_weight [D] or NULL: without it there is
  * no norm behind the block, m = block.  gate [D] or NULL (1).  stream_format:

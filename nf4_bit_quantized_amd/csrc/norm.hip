@@ -2,7 +2,7 @@
 // is normalised for the next layer's input.  Per token, over D channels:
 //   m  = block * r_b,  r_b = 1 / sqrt(mean(block^2) + eps)    (m = block without a norm behind the block)
 //   h' = h + scale * gate * post_weight * m
-//   x  = weight * h' * r,  r = 1 / sqrt(mean(h'^2) + eps)
+//   x  = (h' * r) * weight,  r = 1 / sqrt(mean(h'^2) + eps)
 // x is formed from h' before h' is rounded to the stream's type, rounded once to
 // bf16, or brought straight to the 8-bit form that the 8-bit layer reads (the
 // same rule as k_fp8_quantize_rows, on x in fp32).
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(g[u][e], g[u][e], ss);
     }
-    if (P.post_weight) r_b = 1.0f / sqrtf(block_sum(ss, slot[0]) / (float)P.D + P.eps);
+    if (P.post_weight) r_b = rsqrtf(block_sum(ss, slot[0]) / (float)P.D + P.eps);
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int p = u * step + (int)threadIdx.x;
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
   for (int u = 0; u < NP; ++u)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[u][e], v[u][e], ss);
-  const float r = 1.0f / sqrtf(block_sum(ss, slot[1]) / (float)P.D + P.eps);
+  const float r = rsqrtf(block_sum(ss, slot[1]) / (float)P.D + P.eps);
   if (threadIdx.x == 0) {
     P.stats[2 * (int64_t)blockIdx.x] = r;
     P.stats[2 * (int64_t)blockIdx.x + 1] = r_b;
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormParams P) {
       t.load(P.weight, 8 * p);
       t.values(w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[u][e] *= r * w[e];
+      for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * r * w[e];
       if (P.x) store8<kWeightBf16>(P.x, base + 8 * p, v[u]);
     }
     if (P.codes) {

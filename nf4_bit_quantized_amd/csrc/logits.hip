@@ -44,6 +44,12 @@ struct Sums {
   float m = -kMost, R = -kFar, s = 0.0f, t = 0.0f;
 };
 
+// A sum that has left the range came from logits with |y| above 2^24, where R is
+// not near enough to y for 2^(y - R) to be small (masks of -1e10, say): next to
+// an R that matters it is nothing.  (If there is none, or +inf in the row, the
+// row is read a second time.)  NaN stays.
+__device__ __forceinline__ float in_range(float s) { return s > kMost ? 0.0f : s; }
+
 // Adds N elements; returns the largest of them.
 template <int N, bool ENT>
 __device__ __forceinline__ float add(Sums& a, const float (&f)[N], float c) {
@@ -55,7 +61,7 @@ __device__ __forceinline__ float add(Sums& a, const float (&f)[N], float c) {
   if (y > a.R + 32.0f) {  // sums up to 2^32 times the count stay far inside the range
     const float R = fminf(rintf(y), kFar), d = a.R - R, k = __builtin_amdgcn_exp2f(d);
     if constexpr (ENT) a.t = k > 0.0f ? (a.t + a.s * d) * k : 0.0f;
-    a.s *= k;
+    a.s = in_range(a.s) * k;
     a.R = R;
   }
 #pragma unroll
@@ -221,7 +227,7 @@ __device__ Stats statistics(const Row<F>& row, float c, const int64_t* ids, int 
     block_sum<THREADS>(s, t, sh, r.S, r.T);
   } else {
     const float R = rintf(y), d = a.R - R, k2 = __builtin_amdgcn_exp2f(d);
-    block_sum<THREADS>(a.s * k2, ENT && k2 > 0.0f ? (a.t + a.s * d) * k2 : 0.0f, sh, r.S, r.T);
+    block_sum<THREADS>(in_range(a.s) * k2, ENT && k2 > 0.0f ? (a.t + a.s * d) * k2 : 0.0f, sh, r.S, r.T);
     const double off = (double)R - (double)c * (double)r.M, f = exp2(off);
     if constexpr (ENT) r.T = (r.T + r.S * off) * f;
     r.S *= f;

@@ -502,7 +502,9 @@ int qlora_linear_bwd_checkpoint(const qlora_nf4_desc* d, const uint8_t* packed, 
  * no norm behind the block, m = block.  gate [D] or NULL (1).  stream_format:
  * QLORA_W_F32 or QLORA_W_BF16, of h, h_out, dh_out and dh.  weight_format: the
  * same two, of weight, post_weight and gate.  Sums and statistics are fp32; x
- * is formed from h' before h' is rounded to the stream's type.
+ * is formed from h' before h' is rounded to the stream's type.  The squares
+ * have to stay in fp32's range (block and h' between 1e-16 and 1e16 in size
+ * always do, and zeros with an eps).
  * X: bf16 [T][D] or NULL.  codes, scales: x in the 8-bit form by rows (sizes
  * from qlora_fp8_sizes, from x in fp32), for qlora_fp8_linear_fwd; both NULL
  * or both given; X or they are required.  stats: fp32 [T][2], (r, r_b), for

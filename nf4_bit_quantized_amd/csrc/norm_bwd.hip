@@ -150,7 +150,9 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
       }
     }
     const float mean = s1 * inv;
-    const float mean_p = r_b * r_b * r_b * inv * __builtin_fmaf(-r * mean, s3, s2);  // r_b of c dh m, of m and of dblock
+    // mean(c dh m) r_b, the factor of block in dblock / r_b: from the left, so that each r_b meets a block's size and no
+    // power of it leaves the range
+    const float mean_p = r_b * inv * __builtin_fmaf(-r * mean, s3, s2) * r_b;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int p = u * step + tid;
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           d[e] *= c[e];
-          if constexpr (B == kNormedBlock) d[e] = __builtin_fmaf(-mean_p, m[e], r_b * d[e]);
+          if constexpr (B == kNormedBlock) d[e] = r_b * __builtin_fmaf(-mean_p, m[e], d[e]);
         }
         if (in) store8<kWeightBf16>(P.dblock, t * P.D + 8 * p, d);
       }

@@ -141,8 +141,10 @@ __global__ __launch_bounds__(kThreads) void k_logits_grad(LogitsGradParams P, in
   const float A = sh.A, l2 = 1.44269504f;
   const auto gradient = [&](float z, float w, float a) {
     const float lq = __builtin_fmaf(z - M, scale, -log_s), q = __builtin_amdgcn_exp2f(lq * l2);
-    if (d_H != 0.0f) a = __builtin_fmaf(d_H, fmaxf(lq, -1e30f) + H, a);
-    return scale * __builtin_fmaf(-q, a, w);
+    float g = __builtin_fmaf(-q, a, w);
+    // q first: where it is 0 the term is, however large d_H
+    if (d_H != 0.0f) g = __builtin_fmaf(-d_H, q * (fmaxf(lq, -1e30f) + H), g);
+    return scale * g;
   };
   char* const to = const_cast<char*>(out.start);
   const bool together = in.head == out.head;

@@ -90,3 +90,23 @@ def test_distill(T, V, dtype, rest):
         _alike(sn[t, 2:], [whole, ratio], np.array([F32, 3 * TOL(V) * ratio]), "whole, ratio")
         want, mag = ol.distill_gradient(zn[t], scale, idn[t], vn[t], rest, float(d[t]), *sn[t])
         _near(got[t:t + 1], want[None], mag[None], "dlogits")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("weight", [1e9, -1e20, 1e36])
+def test_large_weights_of_the_entropy(weight, dtype):
+    """A masked token's q is 0, and so is its gradient, at any weight."""
+    import nf4_bit_quantized_amd as q
+    import torch
+    say(f"weight {weight} of the entropy, {dtype}")
+    V = 3000
+    z = _logits(4, V, dtype, seed=12)
+    z[0, ::3] = float("-inf")
+    z[1, V // 2:] = -1e30
+    z[2, 1:] = -200.0
+    _, stats, H, _, _ = q.qlora_token_logprob(z, want_entropy=True)
+    d_H = torch.full((4,), weight, device="cuda")
+    got = q.qlora_token_logprob_bwd(z, None, stats, None, entropy=H, d_entropy=d_H)
+    assert not got[0, ::3].any() and not got[1, V // 2:].any()
+    rows = [ol.score_gradient(_np(z)[t], 1.0, [], [], *_np(stats)[t], float(H[t]), float(d_H[t])) for t in range(4)]
+    _near(got, np.stack([w for w, _ in rows]), np.stack([m for _, m in rows]), "dlogits")

@@ -327,6 +327,10 @@ __device__ void distill_finish(const DistillParams& P, int64_t t, const Listed& 
       r.S += s;
     } else {
       r.T = r.S;
+      if (__ballot(z[0] != z[0] || z[1] != z[1])) {  // nothing but NaN, which no comparison shows
+        r.S = __builtin_nan("");
+        r.M = __builtin_nanf("");
+      }
     }
   }
   const double log_s = log(r.S);

@@ -110,3 +110,25 @@ def test_large_weights_of_the_entropy(weight, dtype):
     assert not got[0, ::3].any() and not got[1, V // 2:].any()
     rows = [ol.score_gradient(_np(z)[t], 1.0, [], [], *_np(stats)[t], float(H[t]), float(d_H[t])) for t in range(4)]
     _near(got, np.stack([w for w, _ in rows]), np.stack([m for _, m in rows]), "dlogits")
+
+
+@pytest.mark.parametrize("V", [6, 300, 20000])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_not_finite_in_the_list_alone(value, V):
+    """Nothing else is left of the row, listed or not: the loss and the gradient are NaN all the same."""
+    import nf4_bit_quantized_amd as q
+    import torch
+    say(f"{value} in the list alone, V {V}")
+    z = torch.full((3, V), float("-inf"), device="cuda")
+    z[0, 2] = float(value)
+    z[1, 1:6] = float(value)
+    z[2, 4] = 1.0
+    ids = torch.arange(1, 6, device="cuda").repeat(3, 1)
+    values = torch.full((3, 5), -2.0, device="cuda")
+    for rest in (False, True):
+        loss, stats = q.qlora_distill_fwd(z, ids, values, rest=rest)
+        got = q.qlora_distill_bwd(z, ids, values, stats, torch.ones(3, device="cuda"), rest=rest)
+        for t in range(3):
+            l, *_ = ol.distill(_np(z)[t], 1.0, ids[t].cpu().numpy(), _np(values)[t], rest)
+            _alike(loss[t].item(), l, 2 * TOL(V), "loss")
+        assert got[:2].isnan().all() and got[2].isfinite().all()

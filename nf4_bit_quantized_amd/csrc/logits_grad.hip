@@ -115,7 +115,9 @@ __device__ void entries(const LogitsGradParams& P, int64_t t, const Row<F>& row,
     }
     n += __popcll(who);
   }
-  const bool idle = __ballot(w[0] != 0.0f || w[1] != 0.0f) == 0 && A == 0.0f && A_listed == 0.0f;
+  // no entries, or none with a weight (d_loss of a row without entries may be anything)
+  const bool idle = __ballot(in[0] || in[1]) == 0 ||
+                    (__ballot(w[0] != 0.0f || w[1] != 0.0f) == 0 && A == 0.0f && A_listed == 0.0f);
   if (lane == 0) {
     sh.count = idle ? -1 : n;
     sh.A = A;

@@ -132,3 +132,20 @@ def test_not_finite_in_the_list_alone(value, V):
             l, *_ = ol.distill(_np(z)[t], 1.0, ids[t].cpu().numpy(), _np(values)[t], rest)
             _alike(loss[t].item(), l, 2 * TOL(V), "loss")
         assert got[:2].isnan().all() and got[2].isfinite().all()
+
+
+def test_rows_without_entries_take_any_weight():
+    import nf4_bit_quantized_amd as q
+    import torch
+    say("rows without entries")
+    z = _logits(3, 500, "float32", seed=13)
+    ids = torch.tensor([[1, 2], [-1, 500], [-100, -1]], device="cuda")
+    values = torch.tensor([[-1.0, -2.0]] * 3, device="cuda")
+    d = torch.tensor([1.0, float("nan"), float("inf")], device="cuda")
+    for rest in (False, True):
+        loss, stats = q.qlora_distill_fwd(z, ids, values, rest=rest)
+        got = q.qlora_distill_bwd(z, ids, values, stats, d, rest=rest)
+        assert not loss[1:].any() and got[0].any() and not got[1:].any()
+    _, stats, _, _, _ = q.qlora_token_logprob(z, ids)
+    got = q.qlora_token_logprob_bwd(z, ids, stats, d[:, None].expand(3, 2).contiguous())
+    assert got[0].any() and not got[1:].any()

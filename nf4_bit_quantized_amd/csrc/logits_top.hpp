@@ -86,8 +86,10 @@ __device__ __forceinline__ void each_element(const Row<F>& row, const At& at) {
 // First the K-th largest value: how many are above a value between the bounds
 // says on which side of it the K-th is, and the nearest elements on both sides
 // of it are the new bounds, so a row of few values is decided in as many passes
-// and any row in 32.  Then all above it, and as many equal to it as are left,
-// in the order of their indexes.
+// and any row in 33: the first value, the end of the limit's own 2^16, may leave
+// out as few as those, and each later one halves what is left.  Then, in two
+// more, all above it, and as many equal to it as are left, in the order of
+// their indexes.
 template <int F, int THREADS>
 __device__ void top_exact(const Row<F>& row, int K, uint32_t low, TopShared<THREADS>& sh) {
   uint32_t high = 0xFFFFFFFFu, mid = low | 0xFFFFu;

@@ -20,12 +20,15 @@
 //
 // Bound by HBM and, near it, by the vector units: five instructions to an
 // element, one of them an exponential that takes four times an ordinary one's
-// cycles, keep the units busy for 82% of the time (90% with alternatives).  4096
-// x 128256 bf16 (1.05 GB): 156 us, 6.7 TB/s; 2048 x 128256 with 64 alternatives
-// 95 us; one row of 128256 8.5 us, of it 3.4 the units of its one CU, 12.4 with
-// twenty alternatives.  More rows in flight or pieces to a thread change one
-// row's time by under 5%; cutting a row over several CUs would take a second
-// launch, whose 2.7 us of host time a call of 12 does not get back.
+// cycles, keep the units busy for 75% of the time (85% with alternatives).  4096
+// x 128256 bf16 (1.05 GB): 156 us, 6.7 TB/s; 2048 x 128256 82 us, with 64
+// alternatives 96; with the entropy, two more instructions to an element, 102
+// (its 1024 threads take 66 registers each in the 16-bit types, so one workgroup
+// to a CU).  One row of 128256 8.8 us, of it 3.4 the units of its one CU, 12.6
+// with twenty alternatives.  More rows in flight or pieces to a thread change
+// one row's time by under 5%; cutting a row over several CUs would take a second
+// launch, whose 2.7 us of host time a call of 12 does not get back (a captured
+// one might).
 #include <type_traits>
 
 #include "logits.hpp"
@@ -393,7 +396,8 @@ float log2_scale(float scale) { return (float)((double)scale * 1.442695040888963
 // Threads to a row, from the row's bytes and the number of rows.  A thread
 // takes four pieces of 16 bytes at a time, so 256, 512 or 1024 threads want
 // 16, 32 or 64 KB of row a round, and what a last round leaves idle counts.  us
-// with 256, 512 and 1024 threads (statistics and one log probability, bf16):
+// with 256, 512 and 1024 threads (statistics and one log probability, bf16,
+// without the entropy, which goes by the same rule):
 //   4096 x 16000   28.5  30.3  48.8        2048 x 64000   47.8  47.4  44.9
 //   4096 x 32000   49.3  47.3  62.7        2048 x 128256  89.9  89.5  85.4
 //   4096 x 50257   73.9  70.7  77.5        77 x 50257 (fp32, five alternatives)  14.4  9.5  12.1

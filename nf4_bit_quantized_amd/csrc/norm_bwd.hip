@@ -13,9 +13,11 @@
 // until the end, and the next token's pieces load while this one's are summed;
 // the workgroups' sums are then added in their order by a second kernel (no
 // atomics).  dx, h', dh' and block are read once, dh and dblock written once.
-// Bound by HBM: 4096 x 8192 bf16 (335 MB) in 56 us with the second kernel's 4, 6.0
+// Bound by HBM: 4096 x 8192 bf16 (335 MB) in 57 us with the second kernel's 5, 5.9
 // TB/s; with a norm behind the block and a gate (403 MB) 76; 1333 x 4096 in fp32
-// with both (98 MB) 26.
+// with both (98 MB) 28, of it 5.6 the second.  Rows of 512 channels and fewer have
+// one wave to a workgroup, 512 waves for 1024 SIMDs: 65536 x 512 bf16 105 us, 3.2
+// TB/s; 32768 x 1024 72, 16384 x 2048 59.
 #include <type_traits>
 
 #include "norm.hpp"
@@ -79,7 +81,11 @@ __device__ __forceinline__ void factors(const NormParams& P, int p, bool in, flo
 
 // NP: pieces of eight channels a thread holds.  With one, its factors stay in
 // registers and the next token's pieces are on their way; with two (more than
-// 8192 channels) there is no room for either.
+// 8192 channels) there is no room for either.  The bound of 1024 threads leaves
+// 128 registers.  With a norm behind the block an fp32 stream spills two of them
+// with one piece; two pieces spill 18 to 23, and three with a gate's gradient and
+// all in fp32: 2048 x 16384 fp32, normed and gated (604 MB), takes 186 us, 3.2
+// TB/s, without either (537 MB) 114.
 template <int FS, int FW, int NP, int B, bool PAST>
 __global__ __launch_bounds__(1024) void k_norm_bwd(NormParams P) {
   __shared__ float4 slot[2][16];  // by token in turn: the one before may still be read

@@ -5,12 +5,13 @@
 //   S = sum exp(scale (z - M)),  log q_j = scale (z_j - M) - log S
 //   H = log S - sum exp(scale (z - M)) scale (z - M) / S
 // One pass over the row: each thread keeps its largest element and, relative to
-// a whole number R near its largest scale * z * log2(e), the sum of 2^(y - R)
-// and for H of 2^(y - R) (y - R), y = c z, c = fl32(scale * log2(e)).  R is
-// whole, so changing from one R to another is exact; y - R is one FMA, rounded
-// once; and the workgroup's result is brought from R to c M in 64 bits with the
-// same c, so nothing that is common to a row is rounded in 32 bits but the
-// terms themselves and their sums.
+// R, at most two below its largest y = c z, c = fl32(scale * log2(e)), the sum of
+// 2^(y - R) and for H of 2^(y - R) (y - R).  y - R is one FMA, rounded once; up
+// to 32 terms are added in 32 bits, in four chains, and the rest in 64; and the
+// workgroup's result is brought from R to c M in 64 bits with the same c.
+// What matters is a row that is sure of its token, where log S and H are small:
+// an element far above the others becomes R itself, so its term, all of S but
+// that little, is put right to 64 bits at the end.
 //
 // A logit of -inf has probability 0.  A row of nothing else has M = -inf,
 // log S = -inf: log probabilities -inf, entropy 0.  NaN or +inf in a row makes
@@ -22,10 +23,9 @@
 // element, one of them an exponential that takes four times an ordinary one's
 // cycles, keep the units busy for 75% of the time (85% with alternatives).  4096
 // x 128256 bf16 (1.05 GB): 156 us, 6.7 TB/s; 2048 x 128256 82 us, with 64
-// alternatives 96; with the entropy, two more instructions to an element, 102
-// (its 1024 threads take 66 registers each in the 16-bit types, so one workgroup
-// to a CU).  One row of 128256 8.8 us, of it 3.4 the units of its one CU, 12.6
-// with twenty alternatives.  More rows in flight or pieces to a thread change
+// alternatives 96; with the entropy, two more instructions to an element, 100.
+// One row of 128256 9.0 us, of it 3.4 the units of its one CU, 13 with twenty
+// alternatives.  More rows in flight or pieces to a thread change
 // one row's time by under 5%; cutting a row over several CUs would take a second
 // launch, whose 2.7 us of host time a call of 12 does not get back (a captured
 // one might).
@@ -43,15 +43,20 @@ using namespace logits;
 
 constexpr float kFar = 1.329227995784916e36f;  // 2^120
 
+// How far a thread's largest y may be above its R, the y of another of its
+// elements: that one is then at least 2^-2 of the largest, and S at least 1.25.
+constexpr float kAbove = 2.0f;
+
 struct Sums {
-  float m = -kMost, R = -kFar, s = 0.0f, t = 0.0f;
+  float m = -kMost, R = -kFar;
+  double s = 0.0, t = 0.0;
 };
 
 // A sum that has left the range came from logits with |y| above 2^24, where R is
 // not near enough to y for 2^(y - R) to be small (masks of -1e10, say): next to
 // an R that matters it is nothing.  (If there is none, or +inf in the row, the
 // row is read a second time.)  NaN stays.
-__device__ __forceinline__ float in_range(float s) { return s > kMost ? 0.0f : s; }
+__device__ __forceinline__ double in_range(double s) { return s > (double)kMost ? 0.0 : s; }
 
 // Adds N elements; returns the largest of them.
 template <int N, bool ENT>
@@ -61,18 +66,32 @@ __device__ __forceinline__ float add(Sums& a, const float (&f)[N], float c) {
   for (int e = 1; e < N; ++e) g = fmaxf(g, f[e]);
   a.m = fmaxf(a.m, g);
   const float y = g * c;
-  if (y > a.R + 32.0f) {  // sums up to 2^32 times the count stay far inside the range
-    const float R = fminf(rintf(y), kFar), d = a.R - R, k = __builtin_amdgcn_exp2f(d);
-    if constexpr (ENT) a.t = k > 0.0f ? (a.t + a.s * d) * k : 0.0f;
+  if (y > a.R + kAbove) {
+    const float R = fminf(y, kFar), d = a.R - R, k = __builtin_amdgcn_exp2f(d);
+    if constexpr (ENT) a.t = k > 0.0f ? (a.t + a.s * d) * k : 0.0;
     a.s = in_range(a.s) * k;
     a.R = R;
   }
+  constexpr int C = N < 4 ? N : 4;
+  float s[C], t[C];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     const float d = __builtin_fmaf(f[e], c, -a.R), x = __builtin_amdgcn_exp2f(d);
-    a.s += x;
-    if constexpr (ENT) a.t = __builtin_fmaf(x, fmaxf(d, -kFar), a.t);  // 0 * -inf stays 0
+    s[e % C] = e < C ? x : s[e % C] + x;
+    if constexpr (ENT) {  // 0 * -inf stays 0
+      const float b = fmaxf(d, -kFar);
+      t[e % C] = e < C ? x * b : __builtin_fmaf(x, b, t[e % C]);
+    }
   }
+#pragma unroll
+  for (int w = 1; w < C; w *= 2)
+#pragma unroll
+    for (int i = 0; i + w < C; i += 2 * w) {
+      s[i] += s[i + w];
+      if constexpr (ENT) t[i] += t[i + w];
+    }
+  a.s += (double)s[0];
+  if constexpr (ENT) a.t += (double)t[0];
   return g;
 }
 
@@ -147,19 +166,20 @@ __device__ __forceinline__ float block_max(float m, Reduced& sh) {
   return v;
 }
 
-template <int THREADS>
-__device__ __forceinline__ void block_sum(float s, float t, Reduced& sh, double& S, double& T) {
-  const double ds = (double)wave::sum(s), dt = (double)wave::sum(t);
+template <bool ENT, int THREADS>
+__device__ __forceinline__ void block_sum(double s, double t, Reduced& sh, double& S, double& T) {
+  s = wave::sum(s);
+  if constexpr (ENT) t = wave::sum(t);
   if ((threadIdx.x & 63) == 0) {
-    sh.s[threadIdx.x >> 6] = ds;
-    sh.t[threadIdx.x >> 6] = dt;
+    sh.s[threadIdx.x >> 6] = s;
+    if constexpr (ENT) sh.t[threadIdx.x >> 6] = t;
   }
   __syncthreads();
   S = T = 0.0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) {
     S += sh.s[w];
-    T += sh.t[w];
+    if constexpr (ENT) T += sh.t[w];
   }
 }
 
@@ -209,11 +229,11 @@ __device__ Stats statistics(const Row<F>& row, float c, const int64_t* ids, int 
   r.M = block_max<THREADS>(a.m, sh);
   const float y = r.M * c;
   if (!(fabsf(y) < 16777216.0f)) {
-    float s = 0.0f, t = 0.0f;
+    double s = 0.0, t = 0.0;
     const auto one = [&](float z) {
       const float d = (z - r.M) * c, x = __builtin_amdgcn_exp2f(d);
-      s += x;
-      if constexpr (ENT) t = __builtin_fmaf(x, fmaxf(d, -kFar), t);
+      s += (double)x;
+      if constexpr (ENT) t += (double)(x * fmaxf(d, -kFar));
     };
     pass([&](int q0, int q1) {
       for (int p = q0 + (int)threadIdx.x; p < q1; p += THREADS) {
@@ -227,11 +247,19 @@ __device__ Stats statistics(const Row<F>& row, float c, const int64_t* ids, int 
       }
     });
     if (mine >= 0) one(z_edge);
-    block_sum<THREADS>(s, t, sh, r.S, r.T);
+    block_sum<ENT, THREADS>(s, t, sh, r.S, r.T);
   } else {
-    const float R = rintf(y), d = a.R - R, k2 = __builtin_amdgcn_exp2f(d);
-    block_sum<THREADS>(in_range(a.s) * k2, ENT && k2 > 0.0f ? (a.t + a.s * d) * k2 : 0.0f, sh, r.S, r.T);
-    const double off = (double)R - (double)c * (double)r.M, f = exp2(off);
+    if (a.m == r.M) {
+      // 2^u in 64 bits in the place of the rounded one; u is what the product rounded, so two terms are enough
+      const float u = __builtin_fmaf(r.M, c, -a.R);
+      if (fabsf(u) < 0x1p-10f) {
+        const double l = 0.6931471805599453 * (double)u;
+        a.s += 1.0 + l + 0.5 * l * l - (double)__builtin_amdgcn_exp2f(u);
+      }
+    }
+    const float d = a.R - y, k2 = __builtin_amdgcn_exp2f(d);
+    block_sum<ENT, THREADS>(in_range(a.s) * k2, ENT && k2 > 0.0f ? (a.t + a.s * d) * k2 : 0.0, sh, r.S, r.T);
+    const double off = (double)y - (double)c * (double)r.M, f = exp2(off);
     if constexpr (ENT) r.T = (r.T + r.S * off) * f;
     r.S *= f;
   }
@@ -245,8 +273,11 @@ __device__ __forceinline__ float log_q(float z, float M, double scale, double lo
   return (float)(scale * ((double)z - (double)M) - log_s);
 }
 
+// With 1024 threads 64 registers each, so that two rows share a CU: 2048 x 128256
+// with the entropy 100 us against 107.  512 threads are faster with the 66 they
+// take then (4096 x 32000: 58 against 60).
 template <int F, bool ENT, int THREADS, int U, bool PAST>
-__global__ __launch_bounds__(THREADS) void k_score(ScoreParams P, float c) {
+__global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 1) void k_score(ScoreParams P, float c) {
   __shared__ Reduced red;
   __shared__ TopShared<THREADS> sh_top;
   __shared__ TopSeen<THREADS> seen;

@@ -13,7 +13,7 @@
 // picked out before the first gradient is stored, so the gradients may take the
 // logits' place; behind a barrier their gradients are written over the common
 // ones, a thread to an entry.  Bound by HBM: 4096 x 128256 bf16 (1.05 GB read,
-// 1.05 written) in 363 us, 5.8 TB/s, where a large copy reaches 5.0.
+// 1.05 written) in 362 us, 5.8 TB/s, where a large copy reaches 5.0.
 //
 // A piece is read whole where the gradient's row starts as far from a 16-byte
 // boundary as the logits' row does, and element by element otherwise: 4096 x
